@@ -311,6 +311,123 @@ int moonep_wgrad(moonep_dims d, int32_t H, int32_t Hp, moonep_dtype t, const voi
 int moonep_reduce_grad(moonep_dims d, int32_t H, int32_t Hp, const int32_t* slot_expert, float* dW_home,
                        float* dW_slots, moonep_stream stream);
 
+/*
+ * Activation checkpoints in 8 bits.  The pages describe a backward pass through the same buffers as the
+ * forward ([P2] "Core technique") and say nothing about what is kept between the two; these calls keep
+ * the two tensors that the gated expert FFN's backward needs, its input and the activation's input, in
+ * 8 bits, and read them there, so that the row buffers of the forward pass are free for the next layer.
+ *
+ * 8-bit rows: a [rows, C] tensor is kept as codes [rows, C] int8 and exps [rows, moonep_save8_blocks(C)]
+ * uint8, one byte per 32 columns of a row (the last one covers what is left).  For a block of columns
+ *   b = max(1, biased float32 exponent of its largest magnitude),  step = 2^(b - 133),
+ *   code = x / step rounded to the nearest even whole number, held within +-127;  value = code * step.
+ * A value is off by at most step / 2 (by step where |x| is within step / 2 of 128 steps), and step is at
+ * most 1/64 of the block's largest magnitude.  x / step and code * step are exact, and every value is a
+ * bfloat16 number.  A block with an infinity or a NaN has b = 255: all its values are NaN, its codes
+ * unspecified.
+ *
+ * In these calls and in the layer norm, output arrays do not overlap inputs or each other; row pointers
+ * need the alignment of their elements only (rows of whole 8-column chunks at 16-byte aligned pointers,
+ * 8 for codes, move fastest).  Widths (C, H, Hp, D) are at most 2^30, the norm's 32768 (MOONEP_EINVAL).
+ */
+
+/* ceil(C / 32): exponent bytes of a row of C columns (0 for C < 1). */
+int32_t moonep_save8_blocks(int32_t C);
+
+/*
+ * moonep_save8 -- rows into 8 bits;  moonep_load8 -- the values that 8-bit rows stand for.
+ * In/Out: X [rows, C] dtype t;  codes [rows, C] int8;  exps [rows, moonep_save8_blocks(C)] uint8.
+ * moonep_load8 writes bf16 and f32 values exactly.  rows >= 0.
+ */
+int moonep_save8(int64_t rows, int32_t C, moonep_dtype t, const void* X, int8_t* codes, uint8_t* exps,
+                 moonep_stream stream);
+int moonep_load8(int64_t rows, int32_t C, moonep_dtype t, const int8_t* codes, const uint8_t* exps, void* X,
+                 moonep_stream stream);
+
+/*
+ * moonep_swiglu_save8 -- moonep_swiglu, and its input kept in 8 bits in the same pass.  Each row's gate and
+ *   up halves are coded as rows of their own: the codes are those of moonep_save8 of Ygu as [2*R*S*K, Hp].
+ * In:  Ygu [R*S*K, 2*Hp] dtype t.
+ * Out: A [R*S*K, Hp] dtype t;  codes [R*S*K, 2, Hp] int8;  exps [R*S*K, 2, moonep_save8_blocks(Hp)] uint8.
+ */
+int moonep_swiglu_save8(moonep_dims d, int32_t Hp, moonep_dtype t, const void* Ygu, void* A, int8_t* codes,
+                        uint8_t* exps, moonep_stream stream);
+
+/*
+ * moonep_swiglu_backward8 -- gradient of moonep_swiglu from its 8-bit input, with the gates applied here
+ *   instead of in combine's backward.  For every row q, with p = src_of_row[q] and w = gates[p]:
+ *     h = silu(g) * u,  A[q] = w * h,  dgates[p] = sum_c dA[q,c] * h[c]  (float32),
+ *     dYgu[q] = w * dA * (u * s * (1 + g * (1 - s)) | g * s),  s = sigmoid(g);
+ *   float32 arithmetic, each result rounded once to dtype t.
+ *   dA is the gradient of the ungated expert output carried through the down projection: dout laid out by
+ *   moonep_combine_backward_ungated and multiplied by W_down^T (moonep_group_gemm_dgrad).  Then
+ *   sum_c dA * h = <dout, Z> is the gate's gradient without Z, and moonep_wgrad of (A, the ungated rows) is
+ *   the down projection's.  src_of_row, gates and dgates may all be NULL: w is then 1.  A row whose
+ *   src_of_row is outside [0, R*S*K) counts as w = 0 and has no dgates; pairs without a row keep theirs.
+ * In:  codes [R*S*K, 2, Hp] int8, exps;  dA [R*S*K, Hp] dtype t;  src_of_row [R*S*K] int32 from moonep_plan;
+ *      gates [R,S,K] float32.
+ * Out: A [R*S*K, Hp], dYgu [R*S*K, 2*Hp] dtype t;  dgates [R,S,K] float32.
+ */
+int moonep_swiglu_backward8(moonep_dims d, int32_t Hp, moonep_dtype t, const int8_t* codes, const uint8_t* exps,
+                            const void* dA, const int32_t* src_of_row, const float* gates, void* A, void* dYgu,
+                            float* dgates, moonep_stream stream);
+
+/*
+ * moonep_dispatch8 -- moonep_dispatch from 8-bit token rows: Xp[dest_idx[r,s,k], :] = v[r,s,:] with
+ *   v = value * gamma + beta (one float32 fused multiply-add per element), rounded once to dtype t; with
+ *   gamma and beta NULL, v = value.  beta alone may be NULL.  Rows with dest -1 are skipped.
+ * In:  codes [R,S,H] int8, exps [R,S,moonep_save8_blocks(H)] uint8;  gamma, beta [H] float32;
+ *      dest_idx [R,S,K] int32.
+ * Out: Xp [R*S*K, H] dtype t.
+ */
+int moonep_dispatch8(moonep_dims d, int32_t H, moonep_dtype t, const int8_t* codes, const uint8_t* exps,
+                     const float* gamma, const float* beta, const int32_t* dest_idx, void* Xp, moonep_stream stream);
+
+/*
+ * moonep_combine_backward_ungated -- the output gradient's rows by expert, without gates:
+ *   dYp[dest_idx[r,s,k], :] = dout[r,s,:], rounded to dtype t; rows with dest -1 are skipped.
+ * In:  dout [R,S,D] float32;  dest_idx [R,S,K] int32.   Out: dYp [R*S*K, D] dtype t.
+ */
+int moonep_combine_backward_ungated(moonep_dims d, int32_t D, moonep_dtype t, const float* dout,
+                                    const int32_t* dest_idx, void* dYp, moonep_stream stream);
+
+/*
+ * Layer norm of the token rows, in front of the expert layer.
+ */
+
+/*
+ * moonep_layernorm -- with m and v the mean and variance (divided by H) of a row x, r = 1 / sqrt(v + eps) and
+ *   z = (x - m) * r:  Y = z * gamma + beta;  float32 arithmetic, rounded once to dtype t.
+ * In:  X [R,S,H] dtype t;  gamma [H] float32;  beta [H] float32 or NULL (0);  eps > 0.
+ * Out: Y [R,S,H] dtype t;  mean [R,S] (m), rstd [R,S] (r) float32, each NULL to skip;
+ *      codes [R,S,H] int8, exps [R,S,moonep_save8_blocks(H)] uint8: z in 8 bits, both NULL to skip.
+ */
+int moonep_layernorm(moonep_dims d, int32_t H, moonep_dtype t, const void* X, const float* gamma, const float* beta,
+                     float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* exps,
+                     moonep_stream stream);
+
+/* Bytes of device workspace moonep_layernorm_backward and moonep_layernorm_backward8 need on the current device. */
+size_t moonep_layernorm_backward_workspace_bytes(moonep_dims d, int32_t H);
+
+/*
+ * moonep_layernorm_backward -- gradients of moonep_layernorm, with gy = dY * gamma and means over a row:
+ *   dX = r * (gy - mean(gy) - z * mean(gy * z));
+ *   dgamma[c] += sum over rows of dY * z;  dbeta[c] += sum over rows of dY  (one addition to what is there).
+ *   float32 sums in a fixed order.  moonep_layernorm_backward forms z from X, mean and rstd,
+ *   moonep_layernorm_backward8 reads it from 8 bits.
+ * In:  dY [R,S,H] float32 (as moonep_dispatch_backward writes it);  X [R,S,H] dtype t and mean [R,S] float32, or
+ *      codes and exps;  rstd [R,S], gamma [H] float32.
+ * Out: dX [R,S,H] float32.   In/Out: dgamma, dbeta [H] float32 (dbeta NULL to skip).
+ * workspace: moonep_layernorm_backward_workspace_bytes(d, H) bytes of device memory (256-byte aligned), contents
+ * ignored on entry.
+ */
+int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype t, const float* dY, const void* X,
+                              const float* mean, const float* rstd, const float* gamma, float* dX, float* dgamma,
+                              float* dbeta, void* workspace, moonep_stream stream);
+int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float* dY, const int8_t* codes, const uint8_t* exps,
+                               const float* rstd, const float* gamma, float* dX, float* dgamma, float* dbeta,
+                               void* workspace, moonep_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,9 +5,13 @@ The C ABI (include/moonep.h) has the seven calls of the layer -- moonep_plan
 moonep_dispatch, moonep_prefetch, moonep_group_gemm, moonep_combine,
 moonep_wgrad, moonep_reduce_grad -- three for the backward of the data path --
 moonep_combine_backward, moonep_group_gemm_dgrad, moonep_dispatch_backward --
-and two for the activation of the gated expert FFN -- moonep_swiglu,
-moonep_swiglu_backward -- exposed here under the same names, taking torch
-tensors.  Importing this
+two for the activation of the gated expert FFN -- moonep_swiglu,
+moonep_swiglu_backward -- three for the layer norm in front of it --
+moonep_layernorm, moonep_layernorm_backward, moonep_layernorm_backward8 -- and
+the 8-bit activation checkpoints -- moonep_save8, moonep_load8,
+moonep_swiglu_save8, moonep_swiglu_backward8, moonep_dispatch8,
+moonep_combine_backward_ungated -- exposed here under the same names, taking
+torch tensors.  Importing this
 package loads libmoonep.so and raises if it is missing; there is no CPU or
 PyTorch fallback.
 """
@@ -19,6 +23,9 @@ from ._lib import (  # noqa: F401
     moonep_dispatch, moonep_prefetch, moonep_group_gemm, moonep_combine, moonep_wgrad, moonep_reduce_grad,
     moonep_combine_backward, moonep_group_gemm_dgrad, moonep_dispatch_backward, moonep_swiglu,
     moonep_swiglu_backward,
+    moonep_save8_blocks, moonep_save8, moonep_load8, moonep_swiglu_save8, moonep_swiglu_backward8, moonep_dispatch8,
+    moonep_combine_backward_ungated, moonep_layernorm, moonep_layernorm_backward_workspace_bytes,
+    moonep_layernorm_backward, moonep_layernorm_backward8,
 )
 from .layer import MoeFFN  # noqa: F401
 from .layer import MoeLayer  # noqa: F401

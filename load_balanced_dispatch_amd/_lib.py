@@ -54,7 +54,7 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python load_balanced_dispatch_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "moonep_last_error": (ctypes.c_char_p, []),
         "moonep_plan_workspace_bytes": (sz, [Dims]),
@@ -75,6 +75,17 @@ def _load():
         "moonep_dispatch_backward": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, vp]),
         "moonep_swiglu": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp]),
         "moonep_swiglu_backward": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, vp]),
+        "moonep_save8_blocks": (i32, [i32]),
+        "moonep_save8": (ctypes.c_int, [i64, i32, ctypes.c_int, vp, vp, vp, vp]),
+        "moonep_load8": (ctypes.c_int, [i64, i32, ctypes.c_int, vp, vp, vp, vp]),
+        "moonep_swiglu_save8": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, vp, vp]),
+        "moonep_swiglu_backward8": (ctypes.c_int, [Dims, i32, ctypes.c_int] + [vp] * 9),
+        "moonep_dispatch8": (ctypes.c_int, [Dims, i32, ctypes.c_int] + [vp] * 7),
+        "moonep_combine_backward_ungated": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, vp]),
+        "moonep_layernorm": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, ctypes.c_float] + [vp] * 6),
+        "moonep_layernorm_backward_workspace_bytes": (sz, [Dims, i32]),
+        "moonep_layernorm_backward": (ctypes.c_int, [Dims, i32, ctypes.c_int] + [vp] * 10),
+        "moonep_layernorm_backward8": (ctypes.c_int, [Dims, i32] + [vp] * 10),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -90,7 +101,10 @@ SYMBOLS = ("moonep_last_error", "moonep_plan_workspace_bytes", "moonep_plan", "m
            "moonep_plan_static_scratch_bytes", "moonep_plan_static", "moonep_dispatch", "moonep_prefetch",
            "moonep_group_gemm_workspace_bytes", "moonep_group_gemm", "moonep_combine",
            "moonep_wgrad_workspace_bytes", "moonep_wgrad", "moonep_reduce_grad", "moonep_combine_backward",
-           "moonep_group_gemm_dgrad", "moonep_dispatch_backward", "moonep_swiglu", "moonep_swiglu_backward")
+           "moonep_group_gemm_dgrad", "moonep_dispatch_backward", "moonep_swiglu", "moonep_swiglu_backward",
+           "moonep_save8_blocks", "moonep_save8", "moonep_load8", "moonep_swiglu_save8", "moonep_swiglu_backward8",
+           "moonep_dispatch8", "moonep_combine_backward_ungated", "moonep_layernorm",
+           "moonep_layernorm_backward_workspace_bytes", "moonep_layernorm_backward", "moonep_layernorm_backward8")
 
 
 def lib():
@@ -318,3 +332,166 @@ def moonep_swiglu_backward(d: Dims, Hp: int, Ygu, dA, dYgu, stream=None):
     _check(_LIB.moonep_swiglu_backward(d, int(Hp), t, _ptr(Ygu, "Ygu", Ygu.dtype, d.N * 2 * Hp),
                                        _ptr(dA, "dA", Ygu.dtype, d.N * Hp),
                                        _ptr(dYgu, "dYgu", Ygu.dtype, d.N * 2 * Hp), _stream(stream)))
+
+
+# ------------------------------------------------------------------ layer norm and 8-bit checkpoints
+
+class _Call:
+    """Checks the tensors of one call, which must all lie on one device, and makes it on that device's current
+    stream (or the one passed), whatever device is current."""
+
+    def __init__(self):
+        self.device = None
+
+    @staticmethod
+    def dtype(t, name):
+        """The row type of a tensor that sets the call's, and the library's code for it."""
+        if t is None:
+            raise ValueError(f"{name} is required")
+        return t.dtype, _dtype_enum(t)
+
+    def ptr(self, t, name, dtype, numel, optional=False):
+        p = _ptr(t, name, dtype, numel, optional)
+        if p is not None:
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the tensors before it on {self.device}")
+        return p
+
+    def workspace(self, t, needed):
+        p = self.ptr(t, "workspace", None, None)
+        if t.numel() * t.element_size() < needed:
+            raise ValueError(f"workspace too small: {needed} bytes needed")
+        return p
+
+    def __call__(self, entry, *args, stream=None):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+        if self.device.index == torch.cuda.current_device():
+            _check(entry(*args, stream.cuda_stream))
+        else:
+            with torch.cuda.device(self.device):
+                _check(entry(*args, stream.cuda_stream))
+
+
+def moonep_save8_blocks(C: int) -> int:
+    """Exponent bytes of an 8-bit row of C columns."""
+    return int(_LIB.moonep_save8_blocks(int(C)))
+
+
+def _codes(c, codes, exps, rows, C, optional=False):
+    """Pointers of 8-bit rows [rows, C]."""
+    import torch
+    return (c.ptr(codes, "codes", torch.int8, rows * C, optional),
+            c.ptr(exps, "exps", torch.uint8, rows * moonep_save8_blocks(C), optional))
+
+
+def moonep_save8(rows: int, C: int, X, codes, exps, stream=None):
+    """Keeps X [rows, C] in 8 bits: codes int8 [rows, C], exps uint8 [rows, moonep_save8_blocks(C)]."""
+    c = _Call()
+    t, code = c.dtype(X, "X")
+    x = c.ptr(X, "X", t, rows * C)
+    c(_LIB.moonep_save8, int(rows), int(C), code, x, *_codes(c, codes, exps, rows, C), stream=stream)
+
+
+def moonep_load8(rows: int, C: int, codes, exps, X, stream=None):
+    """Writes the values of 8-bit rows to X [rows, C] (bfloat16 or float32, both exact)."""
+    c = _Call()
+    t, code = c.dtype(X, "X")
+    x = c.ptr(X, "X", t, rows * C)
+    c(_LIB.moonep_load8, int(rows), int(C), code, *_codes(c, codes, exps, rows, C), x, stream=stream)
+
+
+def moonep_swiglu_save8(d: Dims, Hp: int, Ygu, A, codes, exps, stream=None):
+    """moonep_swiglu, and Ygu kept in 8 bits (its gate and up halves as rows of their own)."""
+    c = _Call()
+    N = d.N
+    t, code = c.dtype(Ygu, "Ygu")
+    y = c.ptr(Ygu, "Ygu", t, N * 2 * Hp)
+    a = c.ptr(A, "A", t, N * Hp)
+    c(_LIB.moonep_swiglu_save8, d, int(Hp), code, y, a, *_codes(c, codes, exps, 2 * N, Hp), stream=stream)
+
+
+def moonep_swiglu_backward8(d: Dims, Hp: int, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, stream=None):
+    """Gradient of moonep_swiglu from its 8-bit input; with src_of_row, gates and dgates (all or none) the gates
+    are applied here: A and dYgu come out times the gate, and dgates is <dA, silu(g) u> per pair."""
+    import torch
+    c = _Call()
+    N = d.N
+    t, code = c.dtype(dA, "dA")
+    rows8 = _codes(c, codes, exps, 2 * N, Hp)
+    c(_LIB.moonep_swiglu_backward8, d, int(Hp), code, *rows8, c.ptr(dA, "dA", t, N * Hp),
+      c.ptr(src_of_row, "src_of_row", torch.int32, N, optional=True),
+      c.ptr(gates, "gates", torch.float32, N, optional=True), c.ptr(A, "A", t, N * Hp),
+      c.ptr(dYgu, "dYgu", t, N * 2 * Hp), c.ptr(dgates, "dgates", torch.float32, N, optional=True), stream=stream)
+
+
+def moonep_dispatch8(d: Dims, H: int, codes, exps, gamma, beta, dest_idx, Xp, stream=None):
+    """moonep_dispatch from 8-bit token rows, times gamma plus beta (float32 [H], or None)."""
+    import torch
+    c = _Call()
+    t, code = c.dtype(Xp, "Xp")
+    rows8 = _codes(c, codes, exps, d.R * d.S, H)
+    c(_LIB.moonep_dispatch8, d, int(H), code, *rows8, c.ptr(gamma, "gamma", torch.float32, H, True),
+      c.ptr(beta, "beta", torch.float32, H, True), c.ptr(dest_idx, "dest_idx", torch.int32, d.N),
+      c.ptr(Xp, "Xp", t, d.N * H), stream=stream)
+
+
+def moonep_combine_backward_ungated(d: Dims, D: int, dout, dest_idx, dYp, stream=None):
+    """The output gradient's rows laid out by expert, without gates."""
+    import torch
+    c = _Call()
+    t, code = c.dtype(dYp, "dYp")
+    c(_LIB.moonep_combine_backward_ungated, d, int(D), code,
+      c.ptr(dout, "dout", torch.float32, d.R * d.S * D), c.ptr(dest_idx, "dest_idx", torch.int32, d.N),
+      c.ptr(dYp, "dYp", t, d.N * D), stream=stream)
+
+
+def moonep_layernorm(d: Dims, H: int, X, gamma, beta, eps: float, Y, mean, rstd, codes=None, exps=None, stream=None):
+    """Layer norm of X [R,S,H]; mean and rstd [R,S] may be None, and codes and exps keep the normalised rows in
+    8 bits."""
+    import torch
+    c = _Call()
+    t, code = c.dtype(X, "X")
+    T, f32 = d.R * d.S, torch.float32
+    c(_LIB.moonep_layernorm, d, int(H), code, c.ptr(X, "X", t, T * H), c.ptr(gamma, "gamma", f32, H),
+      c.ptr(beta, "beta", f32, H, optional=True), float(eps), c.ptr(Y, "Y", t, T * H),
+      c.ptr(mean, "mean", f32, T, optional=True), c.ptr(rstd, "rstd", f32, T, optional=True),
+      *_codes(c, codes, exps, T, H, optional=True), stream=stream)
+
+
+def moonep_layernorm_backward_workspace_bytes(d: Dims, H: int) -> int:
+    return int(_LIB.moonep_layernorm_backward_workspace_bytes(d, int(H)))
+
+
+def _layernorm_backward(c, entry, d, H, dtype, dY, z, rstd, gamma, dX, dgamma, dbeta, workspace, stream):
+    import torch
+    T, f32 = d.R * d.S, torch.float32
+    c(entry, d, int(H), *dtype, c.ptr(dY, "dY", f32, T * H), *z, c.ptr(rstd, "rstd", f32, T),
+      c.ptr(gamma, "gamma", f32, H), c.ptr(dX, "dX", f32, T * H), c.ptr(dgamma, "dgamma", f32, H),
+      c.ptr(dbeta, "dbeta", f32, H, optional=True),
+      c.workspace(workspace, moonep_layernorm_backward_workspace_bytes(d, H)), stream=stream)
+
+
+def moonep_layernorm_backward(d: Dims, H: int, dY, X, mean, rstd, gamma, dX, dgamma, dbeta, workspace, stream=None):
+    """Gradients of moonep_layernorm from its input: writes dX, adds into dgamma and dbeta (or None)."""
+    import torch
+    c = _Call()
+    t, code = c.dtype(X, "X")
+    T = d.R * d.S
+    z = (c.ptr(X, "X", t, T * H), c.ptr(mean, "mean", torch.float32, T))
+    _layernorm_backward(c, _LIB.moonep_layernorm_backward, d, H, (code,), dY, z, rstd, gamma, dX, dgamma,
+                        dbeta, workspace, stream)
+
+
+def moonep_layernorm_backward8(d: Dims, H: int, dY, codes, exps, rstd, gamma, dX, dgamma, dbeta, workspace,
+                               stream=None):
+    """moonep_layernorm_backward from the 8-bit normalised rows."""
+    c = _Call()
+    z = _codes(c, codes, exps, d.R * d.S, H)
+    _layernorm_backward(c, _LIB.moonep_layernorm_backward8, d, H, (), dY, z, rstd, gamma, dX, dgamma, dbeta,
+                        workspace, stream)

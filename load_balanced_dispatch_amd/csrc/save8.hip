@@ -1,0 +1,402 @@
+// 8-bit activation checkpoints of the gated expert FFN and their use in its backward pass.
+//
+// [P2] = "Moonshot open-sources MoonEP: an expert-parallel communication library for MoE training"
+// (umios.umi6.com), section "Core technique": the backward pass runs through the same fixed buffers as
+// the forward.  The pages say nothing about keeping activations in fewer bits; save8.hpp has the format.
+//
+//   save8, load8              rows into 8 bits and back
+//   swiglu_save8              the activation, with its input kept in 8 bits in the same pass
+//   swiglu_backward8          its gradient from that checkpoint, the activation itself (for the down
+//                             projection's weight gradient) and the gates' gradients
+//   dispatch8                 the expert inputs again, from the 8-bit rows of the tokens
+//   combine_backward_ungated  the output gradient's rows by expert, without gates
+//
+// The backward takes the gate out of the output gradient and puts it on the expert's side: with
+// h = silu(g) u, Z = h W and out = sum_k w Z, the gradient of w is <dout, Z> = <dout W^T, h>.  So the
+// ungated rows dout go through the down projection's dgrad, the activation's backward has both factors
+// of that product in registers, and Z need not be kept for it; dW = h^T (w dout) = (w h)^T dout.
+//
+// All are streams over HBM: no value is read or written twice, and a lane moves 8 columns at a time.
+#include "save8.hpp"
+
+namespace moonep {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kMaxBlocks = 1u << 22;  // a launch counts its threads in 32 bits; more work than that is looped over
+
+constexpr int kMaxWidth = 1 << 30;         // column numbers stay clear of 32 bits
+
+unsigned grid_for(int64_t threads) {
+  const int64_t b = (threads + kThreads - 1) / kThreads;
+  return (unsigned)(b < (int64_t)kMaxBlocks ? b : (int64_t)kMaxBlocks);
+}
+
+// ------------------------------------------------------------------ rows
+
+template <typename T, bool AL>
+__global__ __launch_bounds__(kThreads) void save8_rows(const T* __restrict__ X, int8_t* __restrict__ codes,
+                                                       uint8_t* __restrict__ exps, int64_t rows, int C) {
+  const int nb = (C + kBlock8 - 1) / kBlock8;
+  const int64_t total = rows * nb * 4;  // whole quads
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t blk = i >> 2, row = blk / nb;
+    const int col = (int)(blk - row * nb) * kBlock8 + (int)(i & 3) * kChunk;
+    float f[kChunk];
+    load_chunk<AL>(X + row * C, col, C, f);
+    const uint32_t b = block_exponent(f);
+    store_codes<AL>(codes + row * C, col, C, encode(f, b));
+    if ((i & 3) == 0) exps[blk] = (uint8_t)b;
+  }
+}
+
+template <typename T, bool AL>
+__global__ __launch_bounds__(kThreads) void load8_rows(const int8_t* __restrict__ codes,
+                                                       const uint8_t* __restrict__ exps, T* __restrict__ X,
+                                                       int64_t rows, int C) {
+  const int nb = (C + kBlock8 - 1) / kBlock8, nc = chunks8(C);
+  const int64_t total = rows * nc;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / nc;
+    const int c = (int)(i - row * nc), col = c * kChunk;
+    float f[kChunk];
+    decode(load_codes<AL>(codes + row * C, col, C), block_step(exps[row * nb + (c >> 2)]), f);
+    store_chunk<AL>(X + row * C, col, C, f);
+  }
+}
+
+// ------------------------------------------------------------------ activation
+
+// sigmoid from exp of a non-positive argument only, so it never overflows
+__device__ __forceinline__ float sigmoid_f(float g) {
+  const float e = expf(-fabsf(g));
+  const float r = 1.f / (1.f + e);
+  return g >= 0.f ? r : e * r;
+}
+
+template <typename T, bool AL>
+__global__ __launch_bounds__(kThreads) void swiglu_save8_rows(const T* __restrict__ Ygu, T* __restrict__ A,
+                                                              int8_t* __restrict__ codes, uint8_t* __restrict__ exps,
+                                                              int64_t rows, int Hp) {
+  const int nb = (Hp + kBlock8 - 1) / kBlock8;
+  const int64_t total = rows * nb * 4;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t blk = i >> 2, row = blk / nb;
+    const int j = (int)(blk - row * nb), col = j * kBlock8 + (int)(i & 3) * kChunk;
+    float g[kChunk], u[kChunk], a[kChunk];
+    load_chunk<AL>(Ygu + row * 2 * Hp, col, Hp, g);
+    load_chunk<AL>(Ygu + row * 2 * Hp + Hp, col, Hp, u);
+    const uint32_t bg = block_exponent(g), bu = block_exponent(u);
+    store_codes<AL>(codes + row * 2 * Hp, col, Hp, encode(g, bg));
+    store_codes<AL>(codes + row * 2 * Hp + Hp, col, Hp, encode(u, bu));
+    if ((i & 3) == 0) {
+      exps[row * 2 * nb + j] = (uint8_t)bg;
+      exps[row * 2 * nb + nb + j] = (uint8_t)bu;
+    }
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) a[k] = g[k] * sigmoid_f(g[k]) * u[k];
+    store_chunk<AL>(A + row * Hp, col, Hp, a);
+  }
+}
+
+__device__ __forceinline__ float wave_sum_f(float x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+// One wave per row.  The gate's gradient is a chain per lane and a fixed butterfly across the wave, so
+// it does not depend on timing.
+template <typename T, bool AL>
+__global__ __launch_bounds__(kThreads) void swiglu_bwd8_rows(const int8_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ exps,
+                                                             const T* __restrict__ dA,
+                                                             const int32_t* __restrict__ src_of_row,
+                                                             const float* __restrict__ gates, T* __restrict__ A,
+                                                             T* __restrict__ dYgu, float* __restrict__ dgates,
+                                                             int64_t rows, int Hp) {
+  const int lane = threadIdx.x & 63;
+  const int nb = (Hp + kBlock8 - 1) / kBlock8, nc = chunks8(Hp);
+  const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
+  for (int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); row < rows; row += step) {
+    float w = 1.f;
+    int32_t src = -1;
+    if (gates != nullptr) {
+      src = src_of_row[row];
+      const bool ok = src >= 0 && src < rows;
+      w = ok ? gates[src] : 0.f;
+      src = ok ? src : -1;
+    }
+    const int8_t* cr = codes + row * 2 * Hp;
+    const uint8_t* er = exps + row * 2 * nb;
+    float dot = 0.f;
+    for (int c = lane; c < nc; c += 64) {
+      const int col = c * kChunk;
+      float g[kChunk], u[kChunk], d[kChunk], a[kChunk], dg[kChunk], du[kChunk];
+      decode(load_codes<AL>(cr, col, Hp), block_step(er[c >> 2]), g);
+      decode(load_codes<AL>(cr + Hp, col, Hp), block_step(er[nb + (c >> 2)]), u);
+      load_chunk<AL>(dA + row * Hp, col, Hp, d);
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        const float s = sigmoid_f(g[k]), h = g[k] * s * u[k], wd = w * d[k];
+        // past the row's end the codes and dA read as zeros, which a NaN step would not leave so
+        if (AL || col + k < Hp) dot = __builtin_fmaf(d[k], h, dot);
+        a[k] = w * h;
+        dg[k] = wd * u[k] * s * (1.f + g[k] * (1.f - s));
+        du[k] = wd * g[k] * s;
+      }
+      store_chunk<AL>(A + row * Hp, col, Hp, a);
+      store_chunk<AL>(dYgu + row * 2 * Hp, col, Hp, dg);
+      store_chunk<AL>(dYgu + row * 2 * Hp + Hp, col, Hp, du);
+    }
+    if (src >= 0) {
+      dot = wave_sum_f(dot);
+      if (lane == 0) dgates[src] = dot;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dispatch
+
+// A token's chunk from its 8-bit row, times gamma plus beta where they are given.
+template <bool AL>
+struct From8 {
+  const int8_t* codes;
+  const uint8_t* exps;
+  const float* gamma;
+  const float* beta;
+  __device__ __forceinline__ void load(int64_t tok, int col, int C, float (&f)[kChunk]) const {
+    const int nb = (C + kBlock8 - 1) / kBlock8;
+    decode(load_codes<AL>(codes + tok * C, col, C), block_step(exps[tok * nb + col / kBlock8]), f);
+    if (gamma != nullptr) {
+      float w[kChunk], b[kChunk];
+      load_chunk<AL>(gamma, col, C, w);
+      if (beta != nullptr) {
+        load_chunk<AL>(beta, col, C, b);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) b[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) f[i] = __builtin_fmaf(f[i], w[i], b[i]);
+    }
+  }
+};
+
+// A token's chunk from a float32 row.
+template <bool AL>
+struct FromF32 {
+  const float* X;
+  __device__ __forceinline__ void load(int64_t tok, int col, int C, float (&f)[kChunk]) const {
+    load_chunk<AL>(X + tok * C, col, C, f);
+  }
+};
+
+// One wave per 64 chunks of a token's row, read once and stored K times (rows with destination -1 are
+// left out), as the bf16 dispatch does.
+template <typename T, bool AL, bool NT, typename Src>
+__global__ __launch_bounds__(kThreads) void scatter_rows(Src src, const int32_t* __restrict__ dest,
+                                                         T* __restrict__ Xp, int64_t tokens, int K, int C,
+                                                         int pieces) {
+  const int64_t waves = tokens * pieces, step = (int64_t)gridDim.x * (kThreads / 64);
+  for (int64_t g = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); g < waves; g += step) {
+    const int64_t tok = g / pieces;
+    const int col = ((int)(g - tok * pieces) * 64 + (int)(threadIdx.x & 63)) * kChunk;
+    if (col >= C) continue;
+    float f[kChunk];
+    src.load(tok, col, C, f);
+    for (int k = 0; k < K; ++k) {
+      const int32_t d = dest[tok * K + k];
+      if (d >= 0) store_chunk<AL, NT>(Xp + (int64_t)d * C, col, C, f);
+    }
+  }
+}
+
+// Larger outputs go past the caches with non-temporal stores: the bound that the bf16 dispatch measured.
+constexpr int64_t kStreamStoreBytes = int64_t(4) << 30;
+
+template <typename T, bool AL, typename Src>
+void scatter_launch(Src src, const int32_t* dest, void* Xp, const moonep_dims& d, int C, hipStream_t s) {
+  const int64_t tokens = (int64_t)d.R * d.S;
+  const int pieces = (chunks8(C) + 63) / 64;
+  const unsigned grid = grid_for(tokens * pieces * 64);
+  T* out = static_cast<T*>(Xp);
+  if (AL && n_pairs(d) * C * (int64_t)sizeof(T) > kStreamStoreBytes)
+    hipLaunchKernelGGL((scatter_rows<T, AL, AL, Src>), dim3(grid), dim3(kThreads), 0, s, src, dest, out, tokens, d.K,
+                       C, pieces);
+  else
+    hipLaunchKernelGGL((scatter_rows<T, AL, false, Src>), dim3(grid), dim3(kThreads), 0, s, src, dest, out, tokens,
+                       d.K, C, pieces);
+}
+
+template <typename T>
+int rows_launch(const char* name, bool save, int64_t rows, int C, const void* X, const void* codes, const void* exps,
+                void* Xout, hipStream_t s) {
+  const bool al = C % kChunk == 0 && aligned16(save ? X : Xout) && aligned_to(codes, 8);
+  int8_t* c = const_cast<int8_t*>(static_cast<const int8_t*>(codes));
+  uint8_t* e = const_cast<uint8_t*>(static_cast<const uint8_t*>(exps));
+  if (save) {
+    const unsigned grid = grid_for(rows * blocks8(C) * 4);
+    const T* x = static_cast<const T*>(X);
+    if (al) hipLaunchKernelGGL((save8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, C);
+    else hipLaunchKernelGGL((save8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, C);
+  } else {
+    const unsigned grid = grid_for(rows * chunks8(C));
+    T* x = static_cast<T*>(Xout);
+    if (al) hipLaunchKernelGGL((load8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, c, e, x, rows, C);
+    else hipLaunchKernelGGL((load8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, c, e, x, rows, C);
+  }
+  MOONEP_LAUNCH_CHECK(name);
+  return MOONEP_OK;
+}
+
+int check_type(const char* name, moonep_dtype t, const void* a, const void* b) {
+  MOONEP_REQUIRE(t == MOONEP_F32 || t == MOONEP_BF16, "%s: bad dtype %d", name, (int)t);
+  MOONEP_REQUIRE(aligned_to(a, elem_bytes(t)) && aligned_to(b, elem_bytes(t)),
+                 "%s: a row pointer is not aligned to its elements", name);
+  return MOONEP_OK;
+}
+
+int rows_entry(const char* name, bool save, int64_t rows, int32_t C, moonep_dtype t, const void* X, const void* codes,
+               const void* exps, void* Xout, moonep_stream stream) {
+  MOONEP_REQUIRE(rows >= 0, "%s: rows must be >= 0 (got %lld)", name, (long long)rows);
+  MOONEP_REQUIRE(C >= 1 && C <= kMaxWidth, "%s: C must be in [1, 2^30] (got %d)", name, C);
+  MOONEP_REQUIRE(rows <= (int64_t(1) << 56) / C, "%s: rows * C too large", name);
+  const void* x = save ? X : Xout;
+  if (int rc = check_type(name, t, x, nullptr)) return rc;
+  if (rows == 0) return MOONEP_OK;
+  MOONEP_REQUIRE(x && codes && exps, "%s: null pointer", name);
+  hipStream_t s = as_stream(stream);
+  clear_stale_error();
+  return t == MOONEP_BF16 ? rows_launch<uint16_t>(name, save, rows, C, X, codes, exps, Xout, s)
+                          : rows_launch<float>(name, save, rows, C, X, codes, exps, Xout, s);
+}
+
+template <typename T>
+int swiglu_save8_launch(int64_t rows, int Hp, const void* Ygu, void* A, int8_t* codes, uint8_t* exps, hipStream_t s) {
+  const unsigned grid = grid_for(rows * blocks8(Hp) * 4);
+  const T* y = static_cast<const T*>(Ygu);
+  T* a = static_cast<T*>(A);
+  if (Hp % kChunk == 0 && aligned16(Ygu) && aligned16(A) && aligned_to(codes, 8))
+    hipLaunchKernelGGL((swiglu_save8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, y, a, codes, exps, rows, Hp);
+  else
+    hipLaunchKernelGGL((swiglu_save8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, y, a, codes, exps, rows, Hp);
+  MOONEP_LAUNCH_CHECK("moonep_swiglu_save8");
+  return MOONEP_OK;
+}
+
+template <typename T>
+int swiglu_bwd8_launch(int64_t rows, int Hp, const int8_t* codes, const uint8_t* exps, const void* dA,
+                       const int32_t* src_of_row, const float* gates, void* A, void* dYgu, float* dgates,
+                       hipStream_t s) {
+  const unsigned grid = grid_for(rows * 64);
+  const T* d = static_cast<const T*>(dA);
+  T* a = static_cast<T*>(A);
+  T* dy = static_cast<T*>(dYgu);
+  if (Hp % kChunk == 0 && aligned16(dA) && aligned16(A) && aligned16(dYgu) && aligned_to(codes, 8))
+    hipLaunchKernelGGL((swiglu_bwd8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, codes, exps, d, src_of_row,
+                       gates, a, dy, dgates, rows, Hp);
+  else
+    hipLaunchKernelGGL((swiglu_bwd8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, codes, exps, d, src_of_row,
+                       gates, a, dy, dgates, rows, Hp);
+  MOONEP_LAUNCH_CHECK("moonep_swiglu_backward8");
+  return MOONEP_OK;
+}
+
+}  // namespace
+}  // namespace moonep
+
+using namespace moonep;
+
+extern "C" int32_t moonep_save8_blocks(int32_t C) { return C < 1 ? 0 : C / kBlock8 + (C % kBlock8 != 0); }
+
+extern "C" int moonep_save8(int64_t rows, int32_t C, moonep_dtype t, const void* X, int8_t* codes, uint8_t* exps,
+                            moonep_stream stream) {
+  return rows_entry("moonep_save8", true, rows, C, t, X, codes, exps, nullptr, stream);
+}
+
+extern "C" int moonep_load8(int64_t rows, int32_t C, moonep_dtype t, const int8_t* codes, const uint8_t* exps, void* X,
+                            moonep_stream stream) {
+  return rows_entry("moonep_load8", false, rows, C, t, nullptr, codes, exps, X, stream);
+}
+
+extern "C" int moonep_swiglu_save8(moonep_dims d, int32_t Hp, moonep_dtype t, const void* Ygu, void* A, int8_t* codes,
+                                   uint8_t* exps, moonep_stream stream) {
+  const char* name = "moonep_swiglu_save8";
+  if (int rc = check_dims(d, name)) return rc;
+  if (int rc = check_type(name, t, Ygu, A)) return rc;
+  MOONEP_REQUIRE(Hp >= 1 && Hp <= kMaxWidth, "%s: Hp must be in [1, 2^30] (got %d)", name, Hp);
+  const int64_t rows = n_pairs(d);
+  if (rows == 0) return MOONEP_OK;
+  MOONEP_REQUIRE(Ygu && A && codes && exps, "%s: null pointer", name);
+  hipStream_t s = as_stream(stream);
+  clear_stale_error();
+  return t == MOONEP_BF16 ? swiglu_save8_launch<uint16_t>(rows, Hp, Ygu, A, codes, exps, s)
+                          : swiglu_save8_launch<float>(rows, Hp, Ygu, A, codes, exps, s);
+}
+
+extern "C" int moonep_swiglu_backward8(moonep_dims d, int32_t Hp, moonep_dtype t, const int8_t* codes,
+                                       const uint8_t* exps, const void* dA, const int32_t* src_of_row,
+                                       const float* gates, void* A, void* dYgu, float* dgates, moonep_stream stream) {
+  const char* name = "moonep_swiglu_backward8";
+  if (int rc = check_dims(d, name)) return rc;
+  if (int rc = check_type(name, t, dA, A)) return rc;
+  if (int rc = check_type(name, t, dYgu, nullptr)) return rc;
+  MOONEP_REQUIRE(Hp >= 1 && Hp <= kMaxWidth, "%s: Hp must be in [1, 2^30] (got %d)", name, Hp);
+  const int64_t rows = n_pairs(d);
+  if (rows == 0) return MOONEP_OK;
+  MOONEP_REQUIRE(codes && exps && dA && A && dYgu, "%s: null pointer", name);
+  MOONEP_REQUIRE((src_of_row && gates && dgates) || (!src_of_row && !gates && !dgates),
+                 "%s: src_of_row, gates and dgates go together (all given, or all null)", name);
+  hipStream_t s = as_stream(stream);
+  clear_stale_error();
+  return t == MOONEP_BF16
+             ? swiglu_bwd8_launch<uint16_t>(rows, Hp, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, s)
+             : swiglu_bwd8_launch<float>(rows, Hp, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, s);
+}
+
+extern "C" int moonep_dispatch8(moonep_dims d, int32_t H, moonep_dtype t, const int8_t* codes, const uint8_t* exps,
+                                const float* gamma, const float* beta, const int32_t* dest_idx, void* Xp,
+                                moonep_stream stream) {
+  const char* name = "moonep_dispatch8";
+  if (int rc = check_dims(d, name)) return rc;
+  if (int rc = check_type(name, t, Xp, nullptr)) return rc;
+  MOONEP_REQUIRE(H >= 1 && H <= kMaxWidth, "%s: H must be in [1, 2^30] (got %d)", name, H);
+  MOONEP_REQUIRE(gamma || !beta, "%s: beta without gamma", name);
+  if ((int64_t)d.R * d.S == 0) return MOONEP_OK;
+  MOONEP_REQUIRE(codes && exps && dest_idx && Xp, "%s: null pointer", name);
+  hipStream_t s = as_stream(stream);
+  clear_stale_error();
+  const bool al = H % kChunk == 0 && aligned16(Xp) && aligned_to(codes, 8) && aligned16(gamma) && aligned16(beta);
+  if (t == MOONEP_BF16) {
+    if (al) scatter_launch<uint16_t, true>(From8<true>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
+    else scatter_launch<uint16_t, false>(From8<false>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
+  } else {
+    if (al) scatter_launch<float, true>(From8<true>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
+    else scatter_launch<float, false>(From8<false>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
+  }
+  MOONEP_LAUNCH_CHECK(name);
+  return MOONEP_OK;
+}
+
+extern "C" int moonep_combine_backward_ungated(moonep_dims d, int32_t D, moonep_dtype t, const float* dout,
+                                               const int32_t* dest_idx, void* dYp, moonep_stream stream) {
+  const char* name = "moonep_combine_backward_ungated";
+  if (int rc = check_dims(d, name)) return rc;
+  if (int rc = check_type(name, t, dYp, nullptr)) return rc;
+  MOONEP_REQUIRE(D >= 1 && D <= kMaxWidth, "%s: D must be in [1, 2^30] (got %d)", name, D);
+  if ((int64_t)d.R * d.S == 0) return MOONEP_OK;
+  MOONEP_REQUIRE(dout && dest_idx && dYp, "%s: null pointer", name);
+  hipStream_t s = as_stream(stream);
+  clear_stale_error();
+  const bool al = D % kChunk == 0 && aligned16(dout) && aligned16(dYp);
+  if (t == MOONEP_BF16) {
+    if (al) scatter_launch<uint16_t, true>(FromF32<true>{dout}, dest_idx, dYp, d, D, s);
+    else scatter_launch<uint16_t, false>(FromF32<false>{dout}, dest_idx, dYp, d, D, s);
+  } else {
+    if (al) scatter_launch<float, true>(FromF32<true>{dout}, dest_idx, dYp, d, D, s);
+    else scatter_launch<float, false>(FromF32<false>{dout}, dest_idx, dYp, d, D, s);
+  }
+  MOONEP_LAUNCH_CHECK(name);
+  return MOONEP_OK;
+}
