@@ -340,8 +340,10 @@ class _Call:
     """Checks the tensors of one call, which must all lie on one device, and makes it on that device's current
     stream (or the one passed), whatever device is current."""
 
+    __slots__ = ("device",)
+
     def __init__(self):
-        self.device = None
+        self.device = -1  # index, once a tensor has set it
 
     @staticmethod
     def dtype(t, name):
@@ -351,12 +353,14 @@ class _Call:
         return t.dtype, _dtype_enum(t)
 
     def ptr(self, t, name, dtype, numel, optional=False):
-        p = _ptr(t, name, dtype, numel, optional)
-        if p is not None:
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the tensors before it on {self.device}")
+        if t is None and optional:
+            return None
+        p = _ptr(t, name, dtype, numel)
+        device = t.get_device()
+        if device != self.device:
+            if self.device >= 0:
+                raise ValueError(f"{name} is on cuda:{device}, the tensors before it on cuda:{self.device}")
+            self.device = device
         return p
 
     def workspace(self, t, needed):
@@ -368,14 +372,17 @@ class _Call:
     def __call__(self, entry, *args, stream=None):
         import torch
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif stream.device != self.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-        if self.device.index == torch.cuda.current_device():
-            _check(entry(*args, stream.cuda_stream))
+            # the handle alone: torch.cuda.current_stream() costs 2-3 us, as much as a small kernel
+            handle = torch._C._cuda_getCurrentRawStream(self.device)
+        elif stream.device.index != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{self.device}")
+        else:
+            handle = stream.cuda_stream
+        if self.device == torch.cuda.current_device():
+            _check(entry(*args, handle))
         else:
             with torch.cuda.device(self.device):
-                _check(entry(*args, stream.cuda_stream))
+                _check(entry(*args, handle))
 
 
 def moonep_save8_blocks(C: int) -> int:

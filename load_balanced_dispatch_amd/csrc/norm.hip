@@ -7,8 +7,8 @@
 // The forward can write z in 8 bits (save8.hpp) in the same pass; the backward then reads that instead
 // of x, and moonep_dispatch8 makes the expert inputs from it again.
 //
-// A row is read from HBM once and held in registers, 8 columns to a chunk and kNC chunks to a lane, by one wave or
-// by all waves of a block; sums run over lanes with DPP moves, over waves through LDS, always in the same order.
+// A row is read from HBM once and held in registers by one wave or by all waves of a block; sums run over
+// lanes with DPP moves, over waves through LDS, always in the same order.
 #include "save8.hpp"
 
 namespace moonep {
@@ -46,25 +46,52 @@ __device__ __forceinline__ float row_sum(float x, float* lds) {
   return x;
 }
 
-// WAVE: a wave per row, four rows to a block.  Otherwise a block per row.
-template <typename T, bool AL, int NC, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_rows(
-    const T* __restrict__ X, const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
-    T* __restrict__ Y, float* __restrict__ mean, float* __restrict__ rstd, int8_t* __restrict__ codes,
-    uint8_t* __restrict__ exps, int64_t rows, int H) {
+// MAXT = 256: a wave per row, four rows to a block.  Otherwise a block per row.  KEEP: persistent, with gamma and
+// beta in registers from row to row and the next row's loads issued before the current row's stores.
+template <typename T, bool AL, int NC, int MAXT, bool KEEP>
+__global__ __launch_bounds__(MAXT) void layernorm_rows(const T* __restrict__ X, const float* __restrict__ gamma,
+                                                       const float* __restrict__ beta, float eps, T* __restrict__ Y,
+                                                       float* __restrict__ mean, float* __restrict__ rstd,
+                                                       int8_t* __restrict__ codes, uint8_t* __restrict__ exps,
+                                                       int64_t rows, int H) {
+  constexpr bool WAVE = MAXT == 256;
   __shared__ float lds[2][16];
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, lanes = WAVE ? 64 : blockDim.x;
   const int64_t step = WAVE ? (int64_t)gridDim.x * 4 : gridDim.x;
   const int nb = (H + kBlock8 - 1) / kBlock8;
-  for (int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x; row < rows; row += step) {
+  constexpr int NK = KEEP ? NC : 1;
+  float kw[NK][kChunk], kb[NK][kChunk];
+  auto affine = [&](int c, float (&w)[kChunk], float (&b)[kChunk]) {
+    const int col = (c * lanes + t) * kChunk;
+    load_chunk<AL, false>(gamma, col, H, w);
+    if (beta != nullptr) {
+      load_chunk<AL, false>(beta, col, H, b);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) b[i] = 0.f;
+    }
+  };
+  Raw<T> q[NC];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) q[c] = load_raw<AL>(X + row * H, (c * lanes + t) * kChunk, H);
+  };
+  int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (row < rows) load(row);
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) affine(c, kw[c], kb[c]);
+  }
+  for (; row < rows; row += step) {
     float x[NC][kChunk];
     float sum = 0.f, sq = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      load_chunk<AL>(X + row * H, (c * lanes + t) * kChunk, H, x[c]);
+      q[c].unpack(x[c]);
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) sum += x[c][i];
     }
+    if (row + step < rows) load(row + step);
     const float m = row_sum<WAVE>(sum, lds[0]) / (float)H;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -79,7 +106,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_rows(
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int col = (c * lanes + t) * kChunk;
-      float w[kChunk], y[kChunk];
+      float y[kChunk];
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) x[c][i] = x[c][i] * r;
       if (codes != nullptr) {
@@ -87,15 +114,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_rows(
         store_codes<AL>(codes + row * H, col, H, encode(x[c], b));
         if ((t & 3) == 0 && col < H) exps[row * nb + col / kBlock8] = (uint8_t)b;
       }
-      load_chunk<AL>(gamma, col, H, w);
-      if (beta != nullptr) {
-        load_chunk<AL>(beta, col, H, y);
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) y[i] = __builtin_fmaf(x[c][i], kw[c][i], kb[c][i]);
       } else {
+        float w[kChunk];
+        affine(c, w, y);
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) y[i] = 0.f;
+        for (int i = 0; i < kChunk; ++i) y[i] = __builtin_fmaf(x[c][i], w[i], y[i]);
       }
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) y[i] = __builtin_fmaf(x[c][i], w[i], y[i]);
       store_chunk<AL>(Y + row * H, col, H, y);
     }
     if (t == 0) {
@@ -105,85 +132,177 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_rows(
   }
 }
 
-// Where the backward reads z from.
-template <typename T, bool AL>
-struct ZFromX {
-  const T* X;
+// ------------------------------------------------------------------ backward
+//
+// Its rows are float32 (dY and dX), so a lane's chunk is 4 columns: 16 bytes of them, one wide access.
+
+constexpr int kQuad = 4;
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+
+// Columns [col, col + 4) of a float32 row, zeros past its end.
+template <bool AL>
+__device__ __forceinline__ f32x4 load4(const float* p, int col, int H) {
+  f32x4 q = (f32x4)(0.f);
+  if (AL ? col < H : col + kQuad <= H) {
+    if constexpr (AL) q = *reinterpret_cast<const f32x4*>(p + col);
+    else q = *reinterpret_cast<const f32x4_a4*>(p + col);
+  } else if constexpr (!AL) {
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i)
+      if (col + i < H) q[i] = p[col + i];
+  }
+  return q;
+}
+
+template <bool AL>
+__device__ __forceinline__ void store4(float* p, int col, int H, f32x4 q) {
+  if (AL ? col < H : col + kQuad <= H) {
+    if constexpr (AL) *reinterpret_cast<f32x4*>(p + col) = q;
+    else *reinterpret_cast<f32x4_a4*>(p + col) = q;
+  } else if constexpr (!AL) {
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i)
+      if (col + i < H) p[col + i] = q[i];
+  }
+}
+
+// Where the backward reads z from: what it loads for a row and for a chunk, and z from them.  z past the
+// row's end is unspecified (dY is 0 there, and the sums leave it out).
+template <bool AL>
+struct ZFromBf16 {
+  const uint16_t* X;
   const float* mean;
   struct Row {
-    const T* x;
-    float m, r;
+    float m;
   };
-  __device__ __forceinline__ Row row(int64_t i, int H, float r) const { return {X + i * H, mean[i], r}; }
-  __device__ __forceinline__ void load(const Row& q, int col, int H, float (&z)[kChunk]) const {
-    load_chunk<AL>(q.x, col, H, z);
+  typedef u32x2 Chunk;
+  __device__ __forceinline__ Row row(int64_t i) const { return {mean[i]}; }
+  __device__ __forceinline__ Chunk load(int64_t i, int col, int H) const {
+    const uint16_t* p = X + i * H;
+    u32x2 q = {0u, 0u};
+    if (AL ? col < H : col + kQuad <= H) {
+      if constexpr (AL) q = *reinterpret_cast<const u32x2*>(p + col);
+      else q = *reinterpret_cast<const u32x2_a2*>(p + col);
+    } else if constexpr (!AL) {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) z[i] = (z[i] - q.m) * q.r;
+      for (int k = 0; k < kQuad; ++k)
+        if (col + k < H) q[k / 2] |= (uint32_t)p[col + k] << (16 * (k & 1));
+    }
+    return q;
+  }
+  __device__ __forceinline__ f32x4 z(const Chunk& q, const Row& w, float r) const {
+    return {(__uint_as_float(q[0] << 16) - w.m) * r, (__uint_as_float(q[0] & 0xffff0000u) - w.m) * r,
+            (__uint_as_float(q[1] << 16) - w.m) * r, (__uint_as_float(q[1] & 0xffff0000u) - w.m) * r};
+  }
+};
+template <bool AL>
+struct ZFromF32 {
+  const float* X;
+  const float* mean;
+  struct Row {
+    float m;
+  };
+  typedef f32x4 Chunk;
+  __device__ __forceinline__ Row row(int64_t i) const { return {mean[i]}; }
+  __device__ __forceinline__ Chunk load(int64_t i, int col, int H) const { return load4<AL>(X + i * H, col, H); }
+  __device__ __forceinline__ f32x4 z(const Chunk& q, const Row& w, float r) const {
+    return {(q[0] - w.m) * r, (q[1] - w.m) * r, (q[2] - w.m) * r, (q[3] - w.m) * r};
   }
 };
 template <bool AL>
 struct ZFrom8 {
   const int8_t* codes;
   const uint8_t* exps;
-  struct Row {
-    const int8_t* c;
-    const uint8_t* e;
+  struct Row {};
+  struct Chunk {
+    uint32_t q, b;
   };
-  __device__ __forceinline__ Row row(int64_t i, int H, float) const {
-    return {codes + i * H, exps + i * ((H + kBlock8 - 1) / kBlock8)};
-  }
-  __device__ __forceinline__ void load(const Row& q, int col, int H, float (&z)[kChunk]) const {
-    if (col < H) {
-      decode(load_codes<AL>(q.c, col, H), block_step(q.e[col / kBlock8]), z);
-    } else {
+  __device__ __forceinline__ Row row(int64_t) const { return {}; }
+  __device__ __forceinline__ Chunk load(int64_t i, int col, int H) const {
+    const int8_t* p = codes + i * H;
+    Chunk c = {0u, 1u};
+    if (AL ? col < H : col + kQuad <= H) {
+      if constexpr (AL) c.q = *reinterpret_cast<const uint32_t*>(p + col);
+      else c.q = *reinterpret_cast<const u32_a1*>(p + col);
+    } else if constexpr (!AL) {
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) z[i] = 0.f;
+      for (int k = 0; k < kQuad; ++k)
+        if (col + k < H) c.q |= (uint32_t)(uint8_t)p[col + k] << (8 * k);
     }
+    if (col < H) c.b = exps[i * ((H + kBlock8 - 1) / kBlock8) + col / kBlock8];
+    return c;
+  }
+  __device__ __forceinline__ f32x4 z(const Chunk& c, const Row&, float) const {
+    const float s = block_step(c.b);
+    return {(float)(int8_t)c.q * s, (float)(int8_t)(c.q >> 8) * s, (float)(int8_t)(c.q >> 16) * s,
+            (float)(int8_t)(c.q >> 24) * s};
   }
 };
 
 // Persistent: a lane keeps its columns from row to row, and with them gamma and the sums of dy z and dy
-// over the block's rows, which it leaves in part [gridDim.x, 2, H] (WAVE: summed over the four waves).
-template <typename Z, bool AL, int NC, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_bwd_rows(const float* __restrict__ dY, Z src,
+// over its rows, which the block leaves in part [gridDim.x, 2, H] (WAVE: summed over its four waves).
+// The next row's loads are issued before the current row's stores: loads and stores retire in one order,
+// and a load behind the stores would wait for them.
+template <typename Z, bool AL, int NC, int MAXT, bool AHEAD>
+__global__ __launch_bounds__(MAXT) void layernorm_bwd_rows(const float* __restrict__ dY, Z src,
                                                                         const float* __restrict__ rstd,
                                                                         const float* __restrict__ gamma,
                                                                         float* __restrict__ dX,
                                                                         float* __restrict__ part, int64_t rows,
                                                                         int H) {
+  constexpr bool WAVE = MAXT == 256;
+  constexpr bool KEEP = NC < 8;  // gamma in registers
   __shared__ float lds[2][2][16];
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, lanes = WAVE ? 64 : blockDim.x;
   const int64_t step = WAVE ? (int64_t)gridDim.x * 4 : gridDim.x;
-  float w[NC][kChunk], dg[NC][kChunk], db[NC][kChunk];
+  const float inv_h = 1.f / (float)H;
+  f32x4 w[KEEP ? NC : 1], dg[NC], db[NC];
+  auto weight = [&](int c) { return KEEP ? w[KEEP ? c : 0] : load4<AL>(gamma, (c * lanes + t) * kQuad, H); };
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    load_chunk<AL>(gamma, (c * lanes + t) * kChunk, H, w[c]);
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) dg[c][i] = db[c][i] = 0.f;
+    if (KEEP) w[KEEP ? c : 0] = load4<AL>(gamma, (c * lanes + t) * kQuad, H);
+    dg[c] = db[c] = (f32x4)(0.f);
   }
+  struct Loaded {
+    f32x4 dy[NC];
+    typename Z::Chunk q[NC];
+    typename Z::Row row;
+    float r;
+  };
+  auto load = [&](int64_t row, Loaded& a) {
+    a.r = rstd[row];
+    a.row = src.row(row);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * lanes + t) * kQuad;
+      a.dy[c] = load4<AL>(dY + row * H, col, H);
+      a.q[c] = src.load(row, col, H);
+    }
+  };
   int flip = 0;
-  for (int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x; row < rows; row += step) {
-    const float r = rstd[row];
-    const typename Z::Row q = src.row(row, H, r);
-    float dy[NC][kChunk], z[NC][kChunk];
+  int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  Loaded cur, next;
+  if (AHEAD && row < rows) load(row, cur);
+  for (; row < rows; row += step) {
+    if (!AHEAD) load(row, cur);
+    else if (row + step < rows) load(row + step, next);
+    f32x4 z[NC];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * lanes + t) * kChunk;
-      load_chunk<AL>(dY + row * H, col, H, dy[c]);
-      src.load(q, col, H, z[c]);
-    }
+      z[c] = src.z(cur.q[c], cur.row, cur.r);
+      const f32x4 g = weight(c);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        if (!AL && (c * lanes + t) * kChunk + i >= H) z[c][i] = 0.f;
-        const float gy = dy[c][i] * w[c][i];
+      for (int i = 0; i < kQuad; ++i) {
+        if (!AL && (c * lanes + t) * kQuad + i >= H) z[c][i] = 0.f;
+        const float gy = cur.dy[c][i] * g[i];
         s1 += gy;
         s2 = __builtin_fmaf(gy, z[c][i], s2);
-        dg[c][i] = __builtin_fmaf(dy[c][i], z[c][i], dg[c][i]);
-        db[c][i] += dy[c][i];
+        dg[c][i] = __builtin_fmaf(cur.dy[c][i], z[c][i], dg[c][i]);
+        db[c][i] += cur.dy[c][i];
       }
+    }
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if constexpr (!WAVE) {
@@ -201,47 +320,47 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_bwd_rows(const fl
       }
       flip ^= 1;
     }
-    s1 /= (float)H;
-    s2 /= (float)H;
+    s1 *= inv_h;
+    s2 *= inv_h;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * lanes + t) * kChunk;
-      float dx[kChunk];
+      const f32x4 g = weight(c);
+      f32x4 dx;
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) dx[i] = r * (__builtin_fmaf(dy[c][i], w[c][i], -s1) - z[c][i] * s2);
-      store_chunk<AL>(dX + row * H, col, H, dx);
+      for (int i = 0; i < kQuad; ++i)
+        dx[i] = cur.r * (__builtin_fmaf(cur.dy[c][i], g[i], -s1) - z[c][i] * s2);
+      store4<AL>(dX + row * H, (c * lanes + t) * kQuad, H, dx);
     }
+    if (AHEAD) cur = next;
   }
   float* out = part + (int64_t)blockIdx.x * 2 * H;
   if constexpr (WAVE) {
-    __shared__ float fold[3][NC * 64 * kChunk];
+    __shared__ f32x4 fold[3][NC * 64];
     for (int k = 0; k < 2; ++k) {
       if (k) __syncthreads();
       if (threadIdx.x >= 64) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            fold[(threadIdx.x >> 6) - 1][(c * kChunk + i) * 64 + t] = k ? db[c][i] : dg[c][i];
+        for (int c = 0; c < NC; ++c) fold[(threadIdx.x >> 6) - 1][c * 64 + t] = k ? db[c] : dg[c];
       }
       __syncthreads();
       if (threadIdx.x < 64) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c) {
+          const int at = c * 64 + t;
+          f32x4 v = k ? db[c] : dg[c];
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            const int at = (c * kChunk + i) * 64 + t, col = (c * 64 + t) * kChunk + i;
-            const float v = (k ? db[c][i] : dg[c][i]) + fold[0][at] + fold[1][at] + fold[2][at];
-            if (col < H) out[k * H + col] = v;
-          }
+          for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int i = 0; i < kQuad; ++i) v[i] += fold[j][at][i];
+          store4<AL>(out + k * H, at * kQuad, H, v);
+        }
       }
     }
   } else {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * lanes + t) * kChunk;
-      store_chunk<AL>(out, col, H, dg[c]);
-      store_chunk<AL>(out + H, col, H, db[c]);
+      store4<AL>(out, (c * lanes + t) * kQuad, H, dg[c]);
+      store4<AL>(out + H, (c * lanes + t) * kQuad, H, db[c]);
     }
   }
 }
@@ -249,6 +368,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void layernorm_bwd_rows(const fl
 // dgamma += the sum of the blocks' parts, and dbeta: 64 columns to a block, the parts dealt to its
 // 16 waves and their sums added in order.
 constexpr int kFoldWaves = 16;
+constexpr int kFoldBatch = 16;  // parts a lane loads together
 __global__ __launch_bounds__(kFoldWaves * 64) void layernorm_fold(const float* __restrict__ part, int nparts, int H,
                                                                  float* __restrict__ dgamma,
                                                                  float* __restrict__ dbeta) {
@@ -257,8 +377,19 @@ __global__ __launch_bounds__(kFoldWaves * 64) void layernorm_fold(const float* _
   const int col = blockIdx.x * 64 + lane, k = blockIdx.y;
   float* out = k ? dbeta : dgamma;
   float s = 0.f;
-  if (col < H)
-    for (int p = wv; p < nparts; p += kFoldWaves) s += part[((int64_t)p * 2 + k) * H + col];
+  if (col < H) {
+    const float* at = part + (int64_t)k * H + col;
+    for (int p = wv; p < nparts; p += kFoldWaves * kFoldBatch) {
+      float v[kFoldBatch];
+#pragma unroll
+      for (int i = 0; i < kFoldBatch; ++i) {
+        const int q = p + i * kFoldWaves;
+        v[i] = at[(int64_t)(q < nparts ? q : 0) * 2 * H];
+      }
+#pragma unroll
+      for (int i = 0; i < kFoldBatch; ++i) s += p + i * kFoldWaves < nparts ? v[i] : 0.f;
+    }
+  }
   lds[wv][lane] = s;
   __syncthreads();
   if (wv == 0 && col < H) {
@@ -273,47 +404,70 @@ struct RowShape {
   int nc, lanes;
 };
 
-RowShape row_shape(int H) {
+// Forward, chunks of 8 columns.  Two chunks a lane leave room to keep gamma and beta in registers and the next
+// row in flight.  Measured on 32 768 bf16 rows with a checkpoint: 2048 columns 63 us with 2 waves a row
+// against 84 with one wave of 4 chunks and 69 with 4 of 1; 7168 columns 221 us against 273 without
+// keeping anything between rows, and 342 with 14 waves of 1.
+RowShape fwd_shape(int H) {
   const int nch = chunks8(H);
   if (nch <= 64) return {1, 64};
   if (nch <= 128) return {2, 64};
-  if (nch <= 256) return {4, 64};
   if (nch <= 2048) return {2, ((nch + 127) / 128) * 64};
   return {4, ((nch + 255) / 256) * 64};
 }
 
-constexpr int kPartBlocksPerCU = 4;
+// Blocks the forward launches at most, by their waves: three times what runs at a time, so that the last ones
+// fill in (measured: 62 us against 63, 127 against 130 on 2048 and 4096 columns).
+constexpr int kFwdWavesPerCU = 64;
+
+// Backward, chunks of 4 columns.  Measured on 32 768 rows of 7168 columns from the checkpoint: 392 us with 14
+// waves of 2 chunks against 408 with 7 of 4 (128 registers then hold no second row), 422 with 7 of 4
+// loading each row when it is needed; one wave of 4 chunks against 4 of 1 on 1024 columns: 69 us against 93.
+RowShape bwd_shape(int H) {
+  const int nch = (H + kQuad - 1) / kQuad;
+  if (nch <= 64) return {1, 64};
+  if (nch <= 128) return {2, 64};
+  if (nch <= 256) return {4, 64};
+  if (nch <= 2048) return {2, ((nch + 127) / 128) * 64};
+  if (nch <= 4096) return {4, ((nch + 255) / 256) * 64};
+  return {8, ((nch + 511) / 512) * 64};
+}
+
+// Every block of the backward leaves a partial sum of 2 H floats, so it launches fewer than fit: 8 waves to a
+// CU reach the rate of 16 (2048 columns 127 us against 136, 7168 the same), and at least 4 rows to a wave or block.
+constexpr int kBwdWavesPerCU = 8;
+constexpr int kMinRows = 4;
 
 // Blocks of the backward, which are also the partial sums it leaves.
 unsigned bwd_blocks(int64_t rows, const RowShape& q) {
-  const int64_t need = q.lanes == 64 ? (rows + 3) / 4 : rows;
-  const int64_t cap = (int64_t)device_cu_count() * kPartBlocksPerCU;
+  const int64_t groups = q.lanes == 64 ? (rows + 3) / 4 : rows;
+  const int64_t need = (groups + kMinRows - 1) / kMinRows;
+  const int waves = q.lanes == 64 ? 4 : q.lanes / 64;
+  const int64_t cap = (int64_t)device_cu_count() * (waves < kBwdWavesPerCU ? kBwdWavesPerCU / waves : 1);
   return (unsigned)(need < cap ? need : cap);
 }
-
-#define MOONEP_ROW_SHAPES(CALL)                  \
-  if (q.lanes == 64) {                           \
-    if (q.nc == 1) CALL(1, true);                \
-    else if (q.nc == 2) CALL(2, true);           \
-    else CALL(4, true);                          \
-  } else if (q.nc == 2) {                        \
-    CALL(2, false);                              \
-  } else {                                       \
-    CALL(4, false);                              \
-  }
 
 template <typename T, bool AL>
 void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, const float* gamma, const float* beta,
                       float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* exps, hipStream_t s) {
   const int64_t need = q.lanes == 64 ? (rows + 3) / 4 : rows;
-  const unsigned grid = (unsigned)(need < (1 << 22) ? need : (1 << 22));
+  const int waves = q.lanes == 64 ? 4 : q.lanes / 64;
+  const int64_t cap = (int64_t)device_cu_count() * (kFwdWavesPerCU / waves);
+  const unsigned grid = (unsigned)(need < cap ? need : cap);
   const dim3 block(q.lanes == 64 ? 256 : q.lanes);
   const T* x = static_cast<const T*>(X);
   T* y = static_cast<T*>(Y);
-#define MOONEP_LN(NC, WAVE)                                                                                          \
-  hipLaunchKernelGGL((layernorm_rows<T, AL, NC, WAVE>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, mean, rstd, \
-                     codes, exps, rows, H)
-  MOONEP_ROW_SHAPES(MOONEP_LN)
+#define MOONEP_LN(NC, MAXT, KEEP)                                                                               \
+  hipLaunchKernelGGL((layernorm_rows<T, AL, NC, MAXT, KEEP>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, mean, \
+                     rstd, codes, exps, rows, H)
+  if (q.lanes == 64) {
+    if (q.nc == 1) MOONEP_LN(1, 256, true);
+    else MOONEP_LN(2, 256, true);
+  } else if (q.nc == 2) {
+    MOONEP_LN(2, 1024, true);
+  } else {
+    MOONEP_LN(4, 1024, false);
+  }
 #undef MOONEP_LN
 }
 
@@ -321,10 +475,21 @@ template <typename Z, bool AL>
 void layernorm_bwd_launch(const RowShape& q, unsigned grid, int64_t rows, int H, const float* dY, Z z,
                           const float* rstd, const float* gamma, float* dX, float* part, hipStream_t s) {
   const dim3 block(q.lanes == 64 ? 256 : q.lanes);
-#define MOONEP_LNB(NC, WAVE)                                                                                         \
-  hipLaunchKernelGGL((layernorm_bwd_rows<Z, AL, NC, WAVE>), dim3(grid), block, 0, s, dY, z, rstd, gamma, dX, part, \
+#define MOONEP_LNB(NC, MAXT, AHEAD)                                                                                \
+  hipLaunchKernelGGL((layernorm_bwd_rows<Z, AL, NC, MAXT, AHEAD>), dim3(grid), block, 0, s, dY, z, rstd, gamma, dX, part, \
                      rows, H)
-  MOONEP_ROW_SHAPES(MOONEP_LNB)
+  if (q.lanes == 64) {
+    if (q.nc == 1) MOONEP_LNB(1, 256, true);
+    else if (q.nc == 2) MOONEP_LNB(2, 256, true);
+    else MOONEP_LNB(4, 256, true);
+
+  } else if (q.nc == 2) {
+    MOONEP_LNB(2, 1024, true);
+  } else if (q.nc == 4) {
+    MOONEP_LNB(4, 1024, false);
+  } else {
+    MOONEP_LNB(8, 1024, false);
+  }
 #undef MOONEP_LNB
 }
 
@@ -343,7 +508,7 @@ template <typename F>
 int bwd_entry(const char* name, const moonep_dims& d, int32_t H, float* dgamma, float* dbeta, void* workspace,
               hipStream_t s, F go) {
   const int64_t rows = (int64_t)d.R * d.S;
-  const RowShape q = row_shape(H);
+  const RowShape q = bwd_shape(H);
   const unsigned grid = bwd_blocks(rows, q);
   float* part = static_cast<float*>(workspace);
   clear_stale_error();
@@ -375,7 +540,7 @@ extern "C" int moonep_layernorm(moonep_dims d, int32_t H, moonep_dtype t, const 
   MOONEP_REQUIRE(X && gamma && Y, "%s: null pointer", name);
   hipStream_t s = as_stream(stream);
   clear_stale_error();
-  const RowShape q = row_shape(H);
+  const RowShape q = fwd_shape(H);
   const bool al = H % kChunk == 0 && aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
                   aligned_to(codes, 8);
   if (t == MOONEP_BF16) {
@@ -391,7 +556,7 @@ extern "C" int moonep_layernorm(moonep_dims d, int32_t H, moonep_dtype t, const 
 
 extern "C" size_t moonep_layernorm_backward_workspace_bytes(moonep_dims d, int32_t H) {
   if (bwd_checks("moonep_layernorm_backward_workspace_bytes", d, H) != MOONEP_OK) return 0;
-  return (size_t)bwd_blocks((int64_t)d.R * d.S, row_shape(H)) * 2 * H * sizeof(float);
+  return (size_t)bwd_blocks((int64_t)d.R * d.S, bwd_shape(H)) * 2 * H * sizeof(float);
 }
 
 extern "C" int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype t, const float* dY, const void* X,
@@ -405,17 +570,17 @@ extern "C" int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype 
   MOONEP_REQUIRE(dY && X && mean && rstd && gamma && dX && dgamma && workspace, "%s: null pointer", name);
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
-  const bool al = H % kChunk == 0 && aligned16(X) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
+  const bool al = H % kQuad == 0 && aligned_to(X, t == MOONEP_BF16 ? 8 : 16) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
   return bwd_entry(name, d, H, dgamma, dbeta, workspace, s,
                    [&](const RowShape& q, unsigned grid, int64_t rows, float* part) {
                      if (t == MOONEP_BF16) {
                        const uint16_t* x = static_cast<const uint16_t*>(X);
-                       if (al) layernorm_bwd_launch<ZFromX<uint16_t, true>, true>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
-                       else layernorm_bwd_launch<ZFromX<uint16_t, false>, false>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
+                       if (al) layernorm_bwd_launch<ZFromBf16<true>, true>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
+                       else layernorm_bwd_launch<ZFromBf16<false>, false>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
                      } else {
                        const float* x = static_cast<const float*>(X);
-                       if (al) layernorm_bwd_launch<ZFromX<float, true>, true>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
-                       else layernorm_bwd_launch<ZFromX<float, false>, false>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
+                       if (al) layernorm_bwd_launch<ZFromF32<true>, true>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
+                       else layernorm_bwd_launch<ZFromF32<false>, false>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
                      }
                    });
 }
@@ -429,7 +594,7 @@ extern "C" int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float*
   MOONEP_REQUIRE(dY && codes && exps && rstd && gamma && dX && dgamma && workspace, "%s: null pointer", name);
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
-  const bool al = H % kChunk == 0 && aligned_to(codes, 8) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
+  const bool al = H % kQuad == 0 && aligned_to(codes, 4) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
   return bwd_entry(name, d, H, dgamma, dbeta, workspace, s,
                    [&](const RowShape& q, unsigned grid, int64_t rows, float* part) {
                      if (al) layernorm_bwd_launch<ZFrom8<true>, true>(q, grid, rows, H, dY, {codes, exps}, rstd, gamma, dX, part, s);

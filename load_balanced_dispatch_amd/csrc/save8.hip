@@ -67,10 +67,28 @@ __global__ __launch_bounds__(kThreads) void load8_rows(const int8_t* __restrict_
 
 // ------------------------------------------------------------------ activation
 
+// exp(x) for x <= 0 (x far below the last that counts, or infinite, as -200) to about one and a half steps of float32: 2^t with t = x log2(e) rounded, times 1 + ln(2) times
+// what the rounding left out (x log2(e) - t, with log2(e) in two parts).  Below 2^-126 the hardware's 2^t
+// is 0.
+__device__ __forceinline__ float exp_nonpos(float x) {
+  constexpr float kL = 1.44269504f, kLlo = 1.92596299e-8f, kLn2 = 0.693147181f;
+  x = fmaxf(x, -200.f);
+  const float t = x * kL;
+  const float rest = __builtin_fmaf(x, kLlo, __builtin_fmaf(x, kL, -t)) * kLn2;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, rest, e);
+}
+
+// 1 / x for x in [1, 2], to about half a step: the hardware's reciprocal (one step) and a Newton step.
+__device__ __forceinline__ float recip(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  return __builtin_fmaf(__builtin_fmaf(-x, r, 1.f), r, r);
+}
+
 // sigmoid from exp of a non-positive argument only, so it never overflows
 __device__ __forceinline__ float sigmoid_f(float g) {
-  const float e = expf(-fabsf(g));
-  const float r = 1.f / (1.f + e);
+  const float e = exp_nonpos(-fabsf(g));
+  const float r = recip(1.f + e);
   return g >= 0.f ? r : e * r;
 }
 
@@ -105,9 +123,10 @@ __device__ __forceinline__ float wave_sum_f(float x) {
   return x;
 }
 
-// One wave per row.  The gate's gradient is a chain per lane and a fixed butterfly across the wave, so
-// it does not depend on timing.
-template <typename T, bool AL>
+// One wave per row, NC chunks of it to a lane at a time, all of their loads issued before the first is used.
+// The gate's gradient is a chain per lane and a fixed butterfly across the wave, so it does not depend on
+// timing.
+template <typename T, bool AL, int NC>
 __global__ __launch_bounds__(kThreads) void swiglu_bwd8_rows(const int8_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ exps,
                                                              const T* __restrict__ dA,
@@ -119,35 +138,50 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd8_rows(const int8_t* __res
   const int nb = (Hp + kBlock8 - 1) / kBlock8, nc = chunks8(Hp);
   const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
   for (int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); row < rows; row += step) {
-    float w = 1.f;
-    int32_t src = -1;
-    if (gates != nullptr) {
-      src = src_of_row[row];
-      const bool ok = src >= 0 && src < rows;
-      w = ok ? gates[src] : 0.f;
-      src = ok ? src : -1;
-    }
     const int8_t* cr = codes + row * 2 * Hp;
     const uint8_t* er = exps + row * 2 * nb;
-    float dot = 0.f;
-    for (int c = lane; c < nc; c += 64) {
-      const int col = c * kChunk;
-      float g[kChunk], u[kChunk], d[kChunk], a[kChunk], dg[kChunk], du[kChunk];
-      decode(load_codes<AL>(cr, col, Hp), block_step(er[c >> 2]), g);
-      decode(load_codes<AL>(cr + Hp, col, Hp), block_step(er[nb + (c >> 2)]), u);
-      load_chunk<AL>(dA + row * Hp, col, Hp, d);
+    float dot = 0.f, w = 1.f;
+    int32_t src = -1;
+    for (int c0 = lane; c0 - lane < nc; c0 += 64 * NC) {
+      u32x2 qg[NC], qu[NC];
+      uint32_t bg[NC], bu[NC];
+      Raw<T> qd[NC];
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) {
-        const float s = sigmoid_f(g[k]), h = g[k] * s * u[k], wd = w * d[k];
-        // past the row's end the codes and dA read as zeros, which a NaN step would not leave so
-        if (AL || col + k < Hp) dot = __builtin_fmaf(d[k], h, dot);
-        a[k] = w * h;
-        dg[k] = wd * u[k] * s * (1.f + g[k] * (1.f - s));
-        du[k] = wd * g[k] * s;
+      for (int j = 0; j < NC; ++j) {
+        const int c = c0 + 64 * j, col = c * kChunk, blk = min(c >> 2, nb - 1);
+        qg[j] = load_codes<AL>(cr, col, Hp);
+        qu[j] = load_codes<AL>(cr + Hp, col, Hp);
+        qd[j] = load_raw<AL>(dA + row * Hp, col, Hp);
+        bg[j] = er[blk];
+        bu[j] = er[nb + blk];
       }
-      store_chunk<AL>(A + row * Hp, col, Hp, a);
-      store_chunk<AL>(dYgu + row * 2 * Hp, col, Hp, dg);
-      store_chunk<AL>(dYgu + row * 2 * Hp + Hp, col, Hp, du);
+      if (c0 == lane && gates != nullptr) {
+        src = src_of_row[row];
+        const bool ok = src >= 0 && src < rows;
+        w = ok ? gates[src] : 0.f;
+        src = ok ? src : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int col = (c0 + 64 * j) * kChunk;
+        if (col >= Hp) break;
+        float g[kChunk], u[kChunk], d[kChunk], a[kChunk], dg[kChunk], du[kChunk];
+        decode(qg[j], block_step(bg[j]), g);
+        decode(qu[j], block_step(bu[j]), u);
+        qd[j].unpack(d);
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) {
+          const float s = sigmoid_f(g[k]), h = g[k] * s * u[k], wd = w * d[k];
+          // past the row's end the codes and dA read as zeros, which a NaN step would not leave so
+          if (AL || col + k < Hp) dot = __builtin_fmaf(d[k], h, dot);
+          a[k] = w * h;
+          dg[k] = wd * u[k] * s * (1.f + g[k] * (1.f - s));
+          du[k] = wd * g[k] * s;
+        }
+        store_chunk<AL>(A + row * Hp, col, Hp, a);
+        store_chunk<AL>(dYgu + row * 2 * Hp, col, Hp, dg);
+        store_chunk<AL>(dYgu + row * 2 * Hp + Hp, col, Hp, du);
+      }
     }
     if (src >= 0) {
       dot = wave_sum_f(dot);
@@ -170,9 +204,9 @@ struct From8 {
     decode(load_codes<AL>(codes + tok * C, col, C), block_step(exps[tok * nb + col / kBlock8]), f);
     if (gamma != nullptr) {
       float w[kChunk], b[kChunk];
-      load_chunk<AL>(gamma, col, C, w);
+      load_chunk<AL, false>(gamma, col, C, w);
       if (beta != nullptr) {
-        load_chunk<AL>(beta, col, C, b);
+        load_chunk<AL, false>(beta, col, C, b);
       } else {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) b[i] = 0.f;
@@ -194,7 +228,7 @@ struct FromF32 {
 
 // One wave per 64 chunks of a token's row, read once and stored K times (rows with destination -1 are
 // left out), as the bf16 dispatch does.
-template <typename T, bool AL, bool NT, typename Src>
+template <typename T, bool AL, typename Src>
 __global__ __launch_bounds__(kThreads) void scatter_rows(Src src, const int32_t* __restrict__ dest,
                                                          T* __restrict__ Xp, int64_t tokens, int K, int C,
                                                          int pieces) {
@@ -207,26 +241,18 @@ __global__ __launch_bounds__(kThreads) void scatter_rows(Src src, const int32_t*
     src.load(tok, col, C, f);
     for (int k = 0; k < K; ++k) {
       const int32_t d = dest[tok * K + k];
-      if (d >= 0) store_chunk<AL, NT>(Xp + (int64_t)d * C, col, C, f);
+      if (d >= 0) store_chunk<AL>(Xp + (int64_t)d * C, col, C, f);
     }
   }
 }
-
-// Larger outputs go past the caches with non-temporal stores: the bound that the bf16 dispatch measured.
-constexpr int64_t kStreamStoreBytes = int64_t(4) << 30;
 
 template <typename T, bool AL, typename Src>
 void scatter_launch(Src src, const int32_t* dest, void* Xp, const moonep_dims& d, int C, hipStream_t s) {
   const int64_t tokens = (int64_t)d.R * d.S;
   const int pieces = (chunks8(C) + 63) / 64;
   const unsigned grid = grid_for(tokens * pieces * 64);
-  T* out = static_cast<T*>(Xp);
-  if (AL && n_pairs(d) * C * (int64_t)sizeof(T) > kStreamStoreBytes)
-    hipLaunchKernelGGL((scatter_rows<T, AL, AL, Src>), dim3(grid), dim3(kThreads), 0, s, src, dest, out, tokens, d.K,
-                       C, pieces);
-  else
-    hipLaunchKernelGGL((scatter_rows<T, AL, false, Src>), dim3(grid), dim3(kThreads), 0, s, src, dest, out, tokens,
-                       d.K, C, pieces);
+  hipLaunchKernelGGL((scatter_rows<T, AL, Src>), dim3(grid), dim3(kThreads), 0, s, src, dest, static_cast<T*>(Xp), tokens,
+                     d.K, C, pieces);
 }
 
 template <typename T>
@@ -285,20 +311,28 @@ int swiglu_save8_launch(int64_t rows, int Hp, const void* Ygu, void* A, int8_t* 
   return MOONEP_OK;
 }
 
+template <typename T, bool AL, int NC>
+void swiglu_bwd8_go(int64_t rows, int Hp, const int8_t* codes, const uint8_t* exps, const void* dA,
+                    const int32_t* src_of_row, const float* gates, void* A, void* dYgu, float* dgates, hipStream_t s) {
+  hipLaunchKernelGGL((swiglu_bwd8_rows<T, AL, NC>), dim3(grid_for(rows * 64)), dim3(kThreads), 0, s, codes, exps,
+                     static_cast<const T*>(dA), src_of_row, gates, static_cast<T*>(A), static_cast<T*>(dYgu), dgates,
+                     rows, Hp);
+}
+
 template <typename T>
 int swiglu_bwd8_launch(int64_t rows, int Hp, const int8_t* codes, const uint8_t* exps, const void* dA,
                        const int32_t* src_of_row, const float* gates, void* A, void* dYgu, float* dgates,
                        hipStream_t s) {
-  const unsigned grid = grid_for(rows * 64);
-  const T* d = static_cast<const T*>(dA);
-  T* a = static_cast<T*>(A);
-  T* dy = static_cast<T*>(dYgu);
-  if (Hp % kChunk == 0 && aligned16(dA) && aligned16(A) && aligned16(dYgu) && aligned_to(codes, 8))
-    hipLaunchKernelGGL((swiglu_bwd8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, codes, exps, d, src_of_row,
-                       gates, a, dy, dgates, rows, Hp);
-  else
-    hipLaunchKernelGGL((swiglu_bwd8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, codes, exps, d, src_of_row,
-                       gates, a, dy, dgates, rows, Hp);
+  const bool al = Hp % kChunk == 0 && aligned16(dA) && aligned16(A) && aligned16(dYgu) && aligned_to(codes, 8);
+  const int per_lane = (chunks8(Hp) + 63) / 64;
+#define MOONEP_BWD8(AL, NC) \
+  swiglu_bwd8_go<T, AL, NC>(rows, Hp, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, s)
+  if (!al) MOONEP_BWD8(false, 1);
+  else if (per_lane == 1) MOONEP_BWD8(true, 1);
+  else if (per_lane == 2) MOONEP_BWD8(true, 2);
+  else if (per_lane == 3) MOONEP_BWD8(true, 3);
+  else MOONEP_BWD8(true, 4);
+#undef MOONEP_BWD8
   MOONEP_LAUNCH_CHECK("moonep_swiglu_backward8");
   return MOONEP_OK;
 }

@@ -37,76 +37,108 @@ typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 // ------------------------------------------------------------------ chunks of rows
 
-// Element type of a row as stored (bf16 as its 16 bits) and a chunk's wide accesses.
+// A chunk as loaded, by the row's element type (bf16 as its 16 bits): kept packed until it is used, so that
+// a lane can hold several in flight.
 template <typename T>
-struct Elem;
+struct Raw;
 template <>
-struct Elem<uint16_t> {
-  static __device__ __forceinline__ float get(const uint16_t* p) { return bf16_to_f32(*p); }
-  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16(v); }
-  template <bool AL>
-  static __device__ __forceinline__ void load(const uint16_t* p, float (&f)[kChunk]) {
-    u32x4 q;
-    if constexpr (AL) q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+struct Raw<uint16_t> {
+  u32x4 q;
+  __device__ __forceinline__ void zero() { q = (u32x4)(0u); }
+  template <bool AL, bool STREAM>
+  __device__ __forceinline__ void wide(const uint16_t* p) {
+    if constexpr (AL && STREAM) q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    else if constexpr (AL) q = *reinterpret_cast<const u32x4*>(p);
     else q = *reinterpret_cast<const u32x4_a2*>(p);
+  }
+  __device__ __forceinline__ void put(int i, uint16_t v) { q[i / 2] |= (uint32_t)v << (16 * (i & 1)); }
+  __device__ __forceinline__ void unpack(float (&f)[kChunk]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[2 * i] = __uint_as_float(q[i] << 16);
       f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
     }
   }
-  template <bool AL, bool NT>
+};
+template <>
+struct Raw<float> {
+  f32x4 q[2];
+  __device__ __forceinline__ void zero() { q[0] = q[1] = (f32x4)(0.f); }
+  // the two loads read halves of the same lines, which a non-temporal first load would let go of (measured: 5%
+  // slower on float32 rows)
+  template <bool AL, bool STREAM>
+  __device__ __forceinline__ void wide(const float* p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (AL) q[h] = *(reinterpret_cast<const f32x4*>(p) + h);
+      else q[h] = *reinterpret_cast<const f32x4_a4*>(p + 4 * h);
+    }
+  }
+  __device__ __forceinline__ void put(int i, float v) { q[i / 4][i % 4] = v; }
+  __device__ __forceinline__ void unpack(float (&f)[kChunk]) const {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) f[i] = q[i / 4][i % 4];
+  }
+};
+
+// Columns [col, col + 8) of a row of C columns at p, zeros past its end.  STREAM marks what is read once:
+// its loads are non-temporal where they are wide and aligned.
+template <bool AL, bool STREAM = true, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, int col, int C) {
+  Raw<T> r;
+  if (AL ? col < C : col + kChunk <= C) {
+    r.template wide<AL, STREAM>(p + col);
+  } else {
+    r.zero();
+    if constexpr (!AL) {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (col + i < C) r.put(i, p[col + i]);
+    }
+  }
+  return r;
+}
+
+template <bool AL, bool STREAM = true, typename T>
+__device__ __forceinline__ void load_chunk(const T* p, int col, int C, float (&f)[kChunk]) {
+  load_raw<AL, STREAM>(p, col, C).unpack(f);
+}
+
+// Wide and single stores of a chunk.  Aligned bf16 chunks and codes go past the caches: nothing here reads them
+// again, and the streams ran 4-15% faster so; float32 chunks, two stores to the halves of the same lines, 2%
+// slower.
+template <typename T>
+struct Elem;
+template <>
+struct Elem<uint16_t> {
+  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+  template <bool AL>
   static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[kChunk]) {
     u32x4 q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = (uint32_t)f32_to_bf16(f[2 * i]) | ((uint32_t)f32_to_bf16(f[2 * i + 1]) << 16);
-    if constexpr (AL && NT) __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
-    else if constexpr (AL) *reinterpret_cast<u32x4*>(p) = q;
+    if constexpr (AL) __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
     else *reinterpret_cast<u32x4_a2*>(p) = q;
   }
 };
 template <>
 struct Elem<float> {
-  static __device__ __forceinline__ float get(const float* p) { return *p; }
   static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
   template <bool AL>
-  static __device__ __forceinline__ void load(const float* p, float (&f)[kChunk]) {
-    f32x4 q[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (AL) q[h] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + h);
-      else q[h] = *reinterpret_cast<const f32x4_a4*>(p + 4 * h);
-    }
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) f[i] = q[i / 4][i % 4];
-  }
-  template <bool AL, bool NT>
   static __device__ __forceinline__ void store(float* p, const float (&f)[kChunk]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const f32x4 q = {f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
-      if constexpr (AL && NT) __builtin_nontemporal_store(q, reinterpret_cast<f32x4*>(p) + h);
-      else if constexpr (AL) *(reinterpret_cast<f32x4*>(p) + h) = q;
+      if constexpr (AL) *(reinterpret_cast<f32x4*>(p) + h) = q;
       else *reinterpret_cast<f32x4_a4*>(p + 4 * h) = q;
     }
   }
 };
 
-// Columns [col, col + 8) of a row of C columns at p, zeros past its end.
 template <bool AL, typename T>
-__device__ __forceinline__ void load_chunk(const T* p, int col, int C, float (&f)[kChunk]) {
-  if (AL ? col < C : col + kChunk <= C) {
-    Elem<T>::template load<AL>(p + col, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) f[i] = !AL && col + i < C ? Elem<T>::get(p + col + i) : 0.f;
-  }
-}
-
-template <bool AL, bool NT = false, typename T>
 __device__ __forceinline__ void store_chunk(T* p, int col, int C, const float (&f)[kChunk]) {
   if (AL ? col < C : col + kChunk <= C) {
-    Elem<T>::template store<AL, NT>(p + col, f);
+    Elem<T>::template store<AL>(p + col, f);
   } else if constexpr (!AL) {
 #pragma unroll
     for (int i = 0; i < kChunk; ++i)
@@ -119,7 +151,7 @@ template <bool AL>
 __device__ __forceinline__ u32x2 load_codes(const int8_t* p, int col, int C) {
   u32x2 q = {0u, 0u};
   if (AL ? col < C : col + kChunk <= C) {
-    if constexpr (AL) q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + col));
+    if constexpr (AL) q = *reinterpret_cast<const u32x2*>(p + col);
     else q = *reinterpret_cast<const u32x2_a1*>(p + col);
   } else if constexpr (!AL) {
 #pragma unroll
@@ -132,7 +164,7 @@ __device__ __forceinline__ u32x2 load_codes(const int8_t* p, int col, int C) {
 template <bool AL>
 __device__ __forceinline__ void store_codes(int8_t* p, int col, int C, u32x2 q) {
   if (AL ? col < C : col + kChunk <= C) {
-    if constexpr (AL) *reinterpret_cast<u32x2*>(p + col) = q;
+    if constexpr (AL) __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p + col));
     else *reinterpret_cast<u32x2_a1*>(p + col) = q;
   } else if constexpr (!AL) {
 #pragma unroll
