@@ -48,7 +48,7 @@ __device__ __forceinline__ float row_sum(float x, float* lds) {
 
 // MAXT = 256: a wave per row, four rows to a block.  Otherwise a block per row.  KEEP: persistent, with gamma and
 // beta in registers from row to row and the next row's loads issued before the current row's stores.
-template <typename T, bool AL, int NC, int MAXT, bool KEEP>
+template <typename T, bool AL, bool PAST, int NC, int MAXT, bool KEEP>
 __global__ __launch_bounds__(MAXT) void layernorm_rows(const T* __restrict__ X, const float* __restrict__ gamma,
                                                        const float* __restrict__ beta, float eps, T* __restrict__ Y,
                                                        float* __restrict__ mean, float* __restrict__ rstd,
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(MAXT) void layernorm_rows(const T* __restrict__ X, 
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) y[i] = __builtin_fmaf(x[c][i], w[i], y[i]);
       }
-      store_chunk<AL>(Y + row * H, col, H, y);
+      store_chunk<AL, PAST>(Y + row * H, col, H, y);
     }
     if (t == 0) {
       if (mean != nullptr) mean[row] = m;
@@ -447,7 +447,7 @@ unsigned bwd_blocks(int64_t rows, const RowShape& q) {
   return (unsigned)(need < cap ? need : cap);
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool PAST>
 void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, const float* gamma, const float* beta,
                       float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* exps, hipStream_t s) {
   const int64_t need = q.lanes == 64 ? (rows + 3) / 4 : rows;
@@ -458,7 +458,7 @@ void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, con
   const T* x = static_cast<const T*>(X);
   T* y = static_cast<T*>(Y);
 #define MOONEP_LN(NC, MAXT, KEEP)                                                                               \
-  hipLaunchKernelGGL((layernorm_rows<T, AL, NC, MAXT, KEEP>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, mean, \
+  hipLaunchKernelGGL((layernorm_rows<T, AL, PAST, NC, MAXT, KEEP>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, mean, \
                      rstd, codes, exps, rows, H)
   if (q.lanes == 64) {
     if (q.nc == 1) MOONEP_LN(1, 256, true);
@@ -543,13 +543,16 @@ extern "C" int moonep_layernorm(moonep_dims d, int32_t H, moonep_dtype t, const 
   const RowShape q = fwd_shape(H);
   const bool al = H % kChunk == 0 && aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
                   aligned_to(codes, 8);
-  if (t == MOONEP_BF16) {
-    if (al) layernorm_launch<uint16_t, true>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, s);
-    else layernorm_launch<uint16_t, false>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, s);
-  } else {
-    if (al) layernorm_launch<float, true>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, s);
-    else layernorm_launch<float, false>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, s);
-  }
+#define MOONEP_LN(T, AL, PAST) \
+  layernorm_launch<T, AL, PAST>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, s)
+#define MOONEP_LN_BF16(AL, PAST) MOONEP_LN(uint16_t, AL, PAST)
+#define MOONEP_LN_F32(AL, PAST) MOONEP_LN(float, AL, PAST)
+  const int64_t bytes = rows * H * (int64_t)elem_bytes(t);
+  if (t == MOONEP_BF16) MOONEP_BY_ROWS(uint16_t, al, bytes, MOONEP_LN_BF16);
+  else MOONEP_BY_ROWS(float, al, bytes, MOONEP_LN_F32);
+#undef MOONEP_LN
+#undef MOONEP_LN_BF16
+#undef MOONEP_LN_F32
   MOONEP_LAUNCH_CHECK(name);
   return MOONEP_OK;
 }

@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kThreads) void save8_rows(const T* __restrict__ X, 
   }
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool PAST>
 __global__ __launch_bounds__(kThreads) void load8_rows(const int8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ exps, T* __restrict__ X,
                                                        int64_t rows, int C) {
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void load8_rows(const int8_t* __restrict_
     const int c = (int)(i - row * nc), col = c * kChunk;
     float f[kChunk];
     decode(load_codes<AL>(codes + row * C, col, C), block_step(exps[row * nb + (c >> 2)]), f);
-    store_chunk<AL>(X + row * C, col, C, f);
+    store_chunk<AL, PAST>(X + row * C, col, C, f);
   }
 }
 
@@ -92,7 +92,7 @@ __device__ __forceinline__ float sigmoid_f(float g) {
   return g >= 0.f ? r : e * r;
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool PAST>
 __global__ __launch_bounds__(kThreads) void swiglu_save8_rows(const T* __restrict__ Ygu, T* __restrict__ A,
                                                               int8_t* __restrict__ codes, uint8_t* __restrict__ exps,
                                                               int64_t rows, int Hp) {
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_save8_rows(const T* __restric
     }
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) a[k] = g[k] * sigmoid_f(g[k]) * u[k];
-    store_chunk<AL>(A + row * Hp, col, Hp, a);
+    store_chunk<AL, PAST>(A + row * Hp, col, Hp, a);
   }
 }
 
@@ -126,7 +126,7 @@ __device__ __forceinline__ float wave_sum_f(float x) {
 // One wave per row, NC chunks of it to a lane at a time, all of their loads issued before the first is used.
 // The gate's gradient is a chain per lane and a fixed butterfly across the wave, so it does not depend on
 // timing.
-template <typename T, bool AL, int NC>
+template <typename T, bool AL, bool PAST, int NC>
 __global__ __launch_bounds__(kThreads) void swiglu_bwd8_rows(const int8_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ exps,
                                                              const T* __restrict__ dA,
@@ -178,9 +178,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd8_rows(const int8_t* __res
           dg[k] = wd * u[k] * s * (1.f + g[k] * (1.f - s));
           du[k] = wd * g[k] * s;
         }
-        store_chunk<AL>(A + row * Hp, col, Hp, a);
-        store_chunk<AL>(dYgu + row * 2 * Hp, col, Hp, dg);
-        store_chunk<AL>(dYgu + row * 2 * Hp + Hp, col, Hp, du);
+        store_chunk<AL, PAST>(A + row * Hp, col, Hp, a);
+        store_chunk<AL, PAST>(dYgu + row * 2 * Hp, col, Hp, dg);
+        store_chunk<AL, PAST>(dYgu + row * 2 * Hp + Hp, col, Hp, du);
       }
     }
     if (src >= 0) {
@@ -228,7 +228,7 @@ struct FromF32 {
 
 // One wave per 64 chunks of a token's row, read once and stored K times (rows with destination -1 are
 // left out), as the bf16 dispatch does.
-template <typename T, bool AL, typename Src>
+template <typename T, bool AL, bool PAST, typename Src>
 __global__ __launch_bounds__(kThreads) void scatter_rows(Src src, const int32_t* __restrict__ dest,
                                                          T* __restrict__ Xp, int64_t tokens, int K, int C,
                                                          int pieces) {
@@ -241,18 +241,22 @@ __global__ __launch_bounds__(kThreads) void scatter_rows(Src src, const int32_t*
     src.load(tok, col, C, f);
     for (int k = 0; k < K; ++k) {
       const int32_t d = dest[tok * K + k];
-      if (d >= 0) store_chunk<AL>(Xp + (int64_t)d * C, col, C, f);
+      if (d >= 0) store_chunk<AL, PAST>(Xp + (int64_t)d * C, col, C, f);
     }
   }
 }
 
-template <typename T, bool AL, typename Src>
-void scatter_launch(Src src, const int32_t* dest, void* Xp, const moonep_dims& d, int C, hipStream_t s) {
+// Sources are built for aligned rows or any: Src<true> or Src<false>.
+template <typename T, template <bool> class Src, typename... Args>
+void scatter_launch(bool al, const int32_t* dest, void* Xp, const moonep_dims& d, int C, hipStream_t s, Args... args) {
   const int64_t tokens = (int64_t)d.R * d.S;
   const int pieces = (chunks8(C) + 63) / 64;
   const unsigned grid = grid_for(tokens * pieces * 64);
-  hipLaunchKernelGGL((scatter_rows<T, AL, Src>), dim3(grid), dim3(kThreads), 0, s, src, dest, static_cast<T*>(Xp), tokens,
-                     d.K, C, pieces);
+#define MOONEP_SCATTER(AL, PAST)                                                                        \
+  hipLaunchKernelGGL((scatter_rows<T, AL, PAST, Src<AL>>), dim3(grid), dim3(kThreads), 0, s, Src<AL>{args...}, dest, \
+                     static_cast<T*>(Xp), tokens, d.K, C, pieces)
+  MOONEP_BY_ROWS(T, al, n_pairs(d) * C * (int64_t)sizeof(T), MOONEP_SCATTER);
+#undef MOONEP_SCATTER
 }
 
 template <typename T>
@@ -269,8 +273,10 @@ int rows_launch(const char* name, bool save, int64_t rows, int C, const void* X,
   } else {
     const unsigned grid = grid_for(rows * chunks8(C));
     T* x = static_cast<T*>(Xout);
-    if (al) hipLaunchKernelGGL((load8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, c, e, x, rows, C);
-    else hipLaunchKernelGGL((load8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, c, e, x, rows, C);
+#define MOONEP_LOAD8(AL, PAST) \
+  hipLaunchKernelGGL((load8_rows<T, AL, PAST>), dim3(grid), dim3(kThreads), 0, s, c, e, x, rows, C)
+    MOONEP_BY_ROWS(T, al, rows * C * (int64_t)sizeof(T), MOONEP_LOAD8);
+#undef MOONEP_LOAD8
   }
   MOONEP_LAUNCH_CHECK(name);
   return MOONEP_OK;
@@ -303,20 +309,13 @@ int swiglu_save8_launch(int64_t rows, int Hp, const void* Ygu, void* A, int8_t* 
   const unsigned grid = grid_for(rows * blocks8(Hp) * 4);
   const T* y = static_cast<const T*>(Ygu);
   T* a = static_cast<T*>(A);
-  if (Hp % kChunk == 0 && aligned16(Ygu) && aligned16(A) && aligned_to(codes, 8))
-    hipLaunchKernelGGL((swiglu_save8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, y, a, codes, exps, rows, Hp);
-  else
-    hipLaunchKernelGGL((swiglu_save8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, y, a, codes, exps, rows, Hp);
+  const bool al = Hp % kChunk == 0 && aligned16(Ygu) && aligned16(A) && aligned_to(codes, 8);
+#define MOONEP_SAVE8(AL, PAST) \
+  hipLaunchKernelGGL((swiglu_save8_rows<T, AL, PAST>), dim3(grid), dim3(kThreads), 0, s, y, a, codes, exps, rows, Hp)
+  MOONEP_BY_ROWS(T, al, rows * Hp * (int64_t)sizeof(T), MOONEP_SAVE8);
+#undef MOONEP_SAVE8
   MOONEP_LAUNCH_CHECK("moonep_swiglu_save8");
   return MOONEP_OK;
-}
-
-template <typename T, bool AL, int NC>
-void swiglu_bwd8_go(int64_t rows, int Hp, const int8_t* codes, const uint8_t* exps, const void* dA,
-                    const int32_t* src_of_row, const float* gates, void* A, void* dYgu, float* dgates, hipStream_t s) {
-  hipLaunchKernelGGL((swiglu_bwd8_rows<T, AL, NC>), dim3(grid_for(rows * 64)), dim3(kThreads), 0, s, codes, exps,
-                     static_cast<const T*>(dA), src_of_row, gates, static_cast<T*>(A), static_cast<T*>(dYgu), dgates,
-                     rows, Hp);
 }
 
 template <typename T>
@@ -324,15 +323,19 @@ int swiglu_bwd8_launch(int64_t rows, int Hp, const int8_t* codes, const uint8_t*
                        const int32_t* src_of_row, const float* gates, void* A, void* dYgu, float* dgates,
                        hipStream_t s) {
   const bool al = Hp % kChunk == 0 && aligned16(dA) && aligned16(A) && aligned16(dYgu) && aligned_to(codes, 8);
-  const int per_lane = (chunks8(Hp) + 63) / 64;
-#define MOONEP_BWD8(AL, NC) \
-  swiglu_bwd8_go<T, AL, NC>(rows, Hp, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, s)
-  if (!al) MOONEP_BWD8(false, 1);
-  else if (per_lane == 1) MOONEP_BWD8(true, 1);
-  else if (per_lane == 2) MOONEP_BWD8(true, 2);
-  else if (per_lane == 3) MOONEP_BWD8(true, 3);
-  else MOONEP_BWD8(true, 4);
+  const int nc = al ? (chunks8(Hp) + 63) / 64 : 1;
+#define MOONEP_BWD8_NC(AL, PAST, NC)                                                                                 \
+  hipLaunchKernelGGL((swiglu_bwd8_rows<T, AL, PAST, NC>), dim3(grid_for(rows * 64)), dim3(kThreads), 0, s, codes, exps, \
+                     static_cast<const T*>(dA), src_of_row, gates, static_cast<T*>(A), static_cast<T*>(dYgu), dgates, \
+                     rows, Hp)
+#define MOONEP_BWD8(AL, PAST)                       \
+  if (!(AL) || nc == 1) MOONEP_BWD8_NC(AL, PAST, 1); \
+  else if (nc == 2) MOONEP_BWD8_NC(AL, PAST, AL ? 2 : 1); \
+  else if (nc == 3) MOONEP_BWD8_NC(AL, PAST, AL ? 3 : 1); \
+  else MOONEP_BWD8_NC(AL, PAST, AL ? 4 : 1)
+  MOONEP_BY_ROWS(T, al, rows * Hp * (int64_t)sizeof(T), MOONEP_BWD8);
 #undef MOONEP_BWD8
+#undef MOONEP_BWD8_NC
   MOONEP_LAUNCH_CHECK("moonep_swiglu_backward8");
   return MOONEP_OK;
 }
@@ -402,13 +405,8 @@ extern "C" int moonep_dispatch8(moonep_dims d, int32_t H, moonep_dtype t, const 
   hipStream_t s = as_stream(stream);
   clear_stale_error();
   const bool al = H % kChunk == 0 && aligned16(Xp) && aligned_to(codes, 8) && aligned16(gamma) && aligned16(beta);
-  if (t == MOONEP_BF16) {
-    if (al) scatter_launch<uint16_t, true>(From8<true>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
-    else scatter_launch<uint16_t, false>(From8<false>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
-  } else {
-    if (al) scatter_launch<float, true>(From8<true>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
-    else scatter_launch<float, false>(From8<false>{codes, exps, gamma, beta}, dest_idx, Xp, d, H, s);
-  }
+  if (t == MOONEP_BF16) scatter_launch<uint16_t, From8>(al, dest_idx, Xp, d, H, s, codes, exps, gamma, beta);
+  else scatter_launch<float, From8>(al, dest_idx, Xp, d, H, s, codes, exps, gamma, beta);
   MOONEP_LAUNCH_CHECK(name);
   return MOONEP_OK;
 }
@@ -424,13 +422,8 @@ extern "C" int moonep_combine_backward_ungated(moonep_dims d, int32_t D, moonep_
   hipStream_t s = as_stream(stream);
   clear_stale_error();
   const bool al = D % kChunk == 0 && aligned16(dout) && aligned16(dYp);
-  if (t == MOONEP_BF16) {
-    if (al) scatter_launch<uint16_t, true>(FromF32<true>{dout}, dest_idx, dYp, d, D, s);
-    else scatter_launch<uint16_t, false>(FromF32<false>{dout}, dest_idx, dYp, d, D, s);
-  } else {
-    if (al) scatter_launch<float, true>(FromF32<true>{dout}, dest_idx, dYp, d, D, s);
-    else scatter_launch<float, false>(FromF32<false>{dout}, dest_idx, dYp, d, D, s);
-  }
+  if (t == MOONEP_BF16) scatter_launch<uint16_t, FromF32>(al, dest_idx, dYp, d, D, s, dout);
+  else scatter_launch<float, FromF32>(al, dest_idx, dYp, d, D, s, dout);
   MOONEP_LAUNCH_CHECK(name);
   return MOONEP_OK;
 }

@@ -104,27 +104,29 @@ __device__ __forceinline__ void load_chunk(const T* p, int col, int C, float (&f
   load_raw<AL, STREAM>(p, col, C).unpack(f);
 }
 
-// Wide and single stores of a chunk.  Aligned bf16 chunks and codes go past the caches: nothing here reads them
-// again, and the streams ran 4-15% faster so; float32 chunks, two stores to the halves of the same lines, 2%
-// slower.
+// Wide and single stores of a chunk.  PAST writes an aligned bf16 chunk past the caches (float32 chunks, two
+// stores to the halves of the same lines, ran 2% slower so and never do; a template argument, since the compiler
+// makes one ordinary store of a branch between the two kinds).  Codes always go past them: they are
+// read a whole forward pass later.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<uint16_t> {
   static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16(v); }
-  template <bool AL>
+  template <bool AL, bool PAST>
   static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[kChunk]) {
     u32x4 q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = (uint32_t)f32_to_bf16(f[2 * i]) | ((uint32_t)f32_to_bf16(f[2 * i + 1]) << 16);
-    if constexpr (AL) __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
-    else *reinterpret_cast<u32x4_a2*>(p) = q;
+    if constexpr (!AL) *reinterpret_cast<u32x4_a2*>(p) = q;
+    else if constexpr (PAST) __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
+    else *reinterpret_cast<u32x4*>(p) = q;
   }
 };
 template <>
 struct Elem<float> {
   static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-  template <bool AL>
+  template <bool AL, bool PAST>
   static __device__ __forceinline__ void store(float* p, const float (&f)[kChunk]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -135,10 +137,10 @@ struct Elem<float> {
   }
 };
 
-template <bool AL, typename T>
+template <bool AL, bool PAST, typename T>
 __device__ __forceinline__ void store_chunk(T* p, int col, int C, const float (&f)[kChunk]) {
   if (AL ? col < C : col + kChunk <= C) {
-    Elem<T>::template store<AL>(p + col, f);
+    Elem<T>::template store<AL, PAST>(p + col, f);
   } else if constexpr (!AL) {
 #pragma unroll
     for (int i = 0; i < kChunk; ++i)
@@ -219,6 +221,28 @@ __device__ __forceinline__ void decode(u32x2 q, float step, float (&f)[kChunk]) 
 }
 
 // ------------------------------------------------------------------ host side
+
+// Whether rows of type T, `bytes` of them, are written past the caches (PAST).  The call that follows reads it, from the
+// 256 MB last-level cache where it still is there: norm and dispatch of 32 768 x 2048 (134 MB) took 237 us
+// with ordinary stores of the norm's rows and 243 with non-temporal ones, of 32 768 x 7168 (470 MB) 1043 and
+// 1028; alone, the kernels here run 4-15% faster with non-temporal stores.
+template <typename T>
+bool past_caches(bool al, int64_t bytes) {
+  return al && sizeof(T) == 2 && bytes > (int64_t(256) << 20);
+}
+
+// The instantiations a launch chooses from: rows aligned or not, and if aligned and bf16, PAST or not.
+// CALL(AL, PAST) launches one.
+#define MOONEP_BY_ROWS(T, al, bytes, CALL)          \
+  do {                                              \
+    if (past_caches<T>(al, bytes)) {                \
+      CALL(true, (sizeof(T) == 2));                 \
+    } else if (al) {                                \
+      CALL(true, false);                            \
+    } else {                                        \
+      CALL(false, false);                           \
+    }                                               \
+  } while (0)
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
