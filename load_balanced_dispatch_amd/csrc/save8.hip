@@ -67,16 +67,15 @@ __global__ __launch_bounds__(kThreads) void load8_rows(const int8_t* __restrict_
 
 // ------------------------------------------------------------------ activation
 
-// exp(x) for x <= 0 (x far below the last that counts, or infinite, as -200) to about one and a half steps of float32: 2^t with t = x log2(e) rounded, times 1 + ln(2) times
-// what the rounding left out (x log2(e) - t, with log2(e) in two parts).  Below 2^-126 the hardware's 2^t
-// is 0.
+// exp(x) for x <= 0 to about one and a half steps of float32, denormal results included: 2^n 2^f with n the
+// whole number nearest to x log2(e) and f the rest (log2(e) in two parts), so that the hardware's 2^f
+// sees |f| <= 1/2 only.  x far below the last that counts, or infinite, is taken as -200.
 __device__ __forceinline__ float exp_nonpos(float x) {
-  constexpr float kL = 1.44269504f, kLlo = 1.92596299e-8f, kLn2 = 0.693147181f;
+  constexpr float kL = 1.44269504f, kLlo = 1.92596299e-8f;
   x = fmaxf(x, -200.f);
-  const float t = x * kL;
-  const float rest = __builtin_fmaf(x, kLlo, __builtin_fmaf(x, kL, -t)) * kLn2;
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, rest, e);
+  const float n = rintf(x * kL);
+  const float f = __builtin_fmaf(x, kLlo, __builtin_fmaf(x, kL, -n));
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 
 // 1 / x for x in [1, 2], to about half a step: the hardware's reciprocal (one step) and a Newton step.

@@ -152,12 +152,30 @@ class MoeFFN:
     backward -> dgrad and wgrad of the gate|up projection -> dispatch backward -> reduce_grad of both
     projections.  Every buffer has a shape fixed by (R, E, B, S, K, H, H'); nothing depends on the
     routing, so passes allocate nothing.
+
+    `norm=True` puts a layer norm (gamma, beta [H] float32, eps) in front: X is then its input, Xn what the
+    experts see, and backward() continues through it to dX, adding into dgamma and dbeta.
+
+    `save8=True` (with backward=True) keeps only 8 bits of two activations from forward() to backward(): the
+    rows that the experts read (normalised rows with norm=True, else X) in x_codes, x_exps [R, S, ...] and the
+    activation's input Ygu in ygu_codes, ygu_exps.  The row buffers of the forward pass are then free once it
+    is over: they are in the dict `scratch`, which layers of one shape can share by passing one's to the
+    others' constructor (layers sharing it run one after another, as on one stream).  backward() applies the
+    gates on the experts' side: ungated output-gradient rows -> dgrad of the down projection -> swiglu backward
+    from 8 bits (which also gives the gated activation and dgates) -> wgrad of the down projection -> dispatch
+    from 8 bits -> dgrad and wgrad of the gate|up projection -> dispatch backward -> reduce_grad.
     """
 
-    def __init__(self, R, E, B, S, K, H, Hp, dtype=torch.bfloat16, device="cuda", backward=False):
+    def __init__(self, R, E, B, S, K, H, Hp, dtype=torch.bfloat16, device="cuda", backward=False, norm=False,
+                 eps=1e-5, save8=False, scratch=None):
+        if save8 and not backward:
+            raise ValueError("save8 keeps activations for the backward pass: it needs backward=True")
+        if scratch is not None and backward and not save8:
+            raise ValueError("the backward pass reads the row buffers unless save8=True: they cannot be shared")
         self.d: Dims = make_dims(R, E, B, S, K)
         d = self.d
         self.H, self.Hp, self.dtype, self.device = H, Hp, dtype, device
+        self.norm, self.eps, self.save8 = norm, eps, save8
         i32 = dict(dtype=torch.int32, device=device)
         act = dict(dtype=dtype, device=device)
         f32 = dict(dtype=torch.float32, device=device)
@@ -169,30 +187,63 @@ class MoeFFN:
         self.cu_seqlens = torch.zeros((R, E + B + 1), **i32)
         self.slot_expert = torch.full((R, max(B, 0)), -1, **i32)
         self.dest_idx = torch.zeros((R, S, K), **i32)
+        self.src_of_row = torch.zeros(N, **i32) if save8 else None
         self.stats = torch.zeros(4, **i32)
         self.ws_plan = torch.empty(max(1, _lib.moonep_plan_workspace_bytes(d)), dtype=torch.uint8, device=device)
         self.ws_gemm = torch.empty(max(1, _lib.moonep_group_gemm_workspace_bytes(d)), dtype=torch.uint8,
                                    device=device)
         self.X = torch.zeros((R, S, H), **act)
-        self.Xp = torch.empty((N, H), **act)
+        if norm:
+            self.gamma = torch.ones(H, **f32)
+            self.beta = torch.zeros(H, **f32)
+            self.Xn = torch.empty((R, S, H), **act)
+            self.mean = torch.empty((R, S), **f32)
+            self.rstd = torch.empty((R, S), **f32)
+        else:
+            self.Xn = self.X
+        rows = {"Xp": (N, H), "Ygu": (N, 2 * Hp), "A": (N, Hp), "Zp": (N, H)}
+        if save8:  # the backward's rows of these shapes take the places of Zp and Ygu
+            rows.update(dA=(N, Hp), dXp=(N, H))
+        if scratch is None:
+            scratch = {name: torch.empty(shape, **act) for name, shape in rows.items()}
+        for name, shape in rows.items():
+            t = scratch.get(name)
+            if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"scratch must hold {name} {list(shape)} {dtype}")
+        self.scratch = scratch
+        self.Xp, self.Ygu, self.A, self.Zp = (scratch[name] for name in ("Xp", "Ygu", "A", "Zp"))
         self.W_gu_home = torch.zeros((E, H, 2 * Hp), **act)
         self.W_gu_slots = torch.zeros((R, B, H, 2 * Hp), **act)
         self.W_down_home = torch.zeros((E, Hp, H), **act)
         self.W_down_slots = torch.zeros((R, B, Hp, H), **act)
-        self.Ygu = torch.empty((N, 2 * Hp), **act)
-        self.A = torch.empty((N, Hp), **act)
-        self.Zp = torch.empty((N, H), **act)
         self.out = torch.empty((R, S, H), **f32)
+        if save8:
+            codes = lambda *shape: (torch.empty(shape, dtype=torch.int8, device=device),  # noqa: E731
+                                    torch.empty(shape[:-1] + (_lib.moonep_save8_blocks(shape[-1]),),
+                                                dtype=torch.uint8, device=device))
+            self.x_codes, self.x_exps = codes(R, S, H)
+            self.ygu_codes, self.ygu_exps = codes(N, 2, Hp)
         if backward:
             self.ws_wgrad = torch.empty(max(1, _lib.moonep_wgrad_workspace_bytes(d)), dtype=torch.uint8,
                                         device=device)
             self.dout = torch.zeros((R, S, H), **f32)
             self.dgates = torch.zeros((R, S, K), **f32)
-            self.dZp = torch.empty((N, H), **act)
-            self.dA = torch.empty((N, Hp), **act)
-            self.dYgu = torch.empty((N, 2 * Hp), **act)
-            self.dXp = torch.empty((N, H), **act)
+            if save8:
+                self.dZp, self.dYgu, self.dA, self.dXp = self.Zp, self.Ygu, scratch["dA"], scratch["dXp"]
+            else:
+                self.dZp = torch.empty((N, H), **act)
+                self.dA = torch.empty((N, Hp), **act)
+                self.dYgu = torch.empty((N, 2 * Hp), **act)
+                self.dXp = torch.empty((N, H), **act)
             self.dX = torch.empty((R, S, H), **f32)
+            if norm:
+                self.dXn = torch.empty((R, S, H), **f32)
+                self.dgamma = torch.zeros(H, **f32)
+                self.dbeta = torch.zeros(H, **f32)
+                self.ws_norm = torch.empty(max(1, _lib.moonep_layernorm_backward_workspace_bytes(d, H)),
+                                           dtype=torch.uint8, device=device)
+            else:
+                self.dXn = self.dX
             self.dW_gu_home = torch.zeros((E, H, 2 * Hp), **f32)
             self.dW_gu_slots = torch.zeros((R, B, H, 2 * Hp), **f32)
             self.dW_down_home = torch.zeros((E, Hp, H), **f32)
@@ -204,45 +255,84 @@ class MoeFFN:
     def forward_calls(self):
         d, H, Hp, L = self.d, self.H, self.Hp, _lib
         sl = self._slots
-        return [
+        calls = [
             ("plan", lambda: L.moonep_plan(d, self.topk_idx, self.expert_counts, self.maxvio, self.cu_seqlens,
-                                           sl(self.slot_expert), self.dest_idx, None, self.stats, self.ws_plan)),
+                                           sl(self.slot_expert), self.dest_idx, self.src_of_row, self.stats,
+                                           self.ws_plan)),
             ("prefetch", lambda: (L.moonep_prefetch(d, H, 2 * Hp, self.W_gu_home, sl(self.slot_expert),
                                                     sl(self.W_gu_slots)),
                                   L.moonep_prefetch(d, Hp, H, self.W_down_home, sl(self.slot_expert),
                                                     sl(self.W_down_slots)))),
-            ("dispatch", lambda: L.moonep_dispatch(d, H, self.X, self.dest_idx, self.Xp)),
+        ]
+        if self.norm:
+            calls.append(("layernorm", lambda: L.moonep_layernorm(
+                d, H, self.X, self.gamma, self.beta, self.eps, self.Xn, self.mean, self.rstd,
+                self.x_codes if self.save8 else None, self.x_exps if self.save8 else None)))
+        elif self.save8:
+            calls.append(("save8", lambda: L.moonep_save8(d.R * d.S, H, self.X, self.x_codes, self.x_exps)))
+        calls += [
+            ("dispatch", lambda: L.moonep_dispatch(d, H, self.Xn, self.dest_idx, self.Xp)),
             ("gemm_gate_up", lambda: L.moonep_group_gemm(d, H, 2 * Hp, self.Xp, self.W_gu_home, sl(self.W_gu_slots),
                                                          self.cu_seqlens, self.Ygu, self.ws_gemm)),
-            ("swiglu", lambda: L.moonep_swiglu(d, Hp, self.Ygu, self.A)),
+            ("swiglu_save8", lambda: L.moonep_swiglu_save8(d, Hp, self.Ygu, self.A, self.ygu_codes, self.ygu_exps))
+            if self.save8 else ("swiglu", lambda: L.moonep_swiglu(d, Hp, self.Ygu, self.A)),
             ("gemm_down", lambda: L.moonep_group_gemm(d, Hp, H, self.A, self.W_down_home, sl(self.W_down_slots),
                                                       self.cu_seqlens, self.Zp, self.ws_gemm)),
             ("combine", lambda: L.moonep_combine(d, H, self.Zp, self.dest_idx, self.gates, self.out)),
         ]
+        return calls
 
     def backward_calls(self):
         d, H, Hp, L = self.d, self.H, self.Hp, _lib
         sl = self._slots
-        return [
-            ("combine_backward", lambda: L.moonep_combine_backward(d, H, self.dout, self.Zp, self.dest_idx,
-                                                                   self.gates, self.dZp, self.dgates)),
-            ("dgrad_down", lambda: L.moonep_group_gemm_dgrad(d, Hp, H, self.dZp, self.W_down_home,
-                                                             sl(self.W_down_slots), self.cu_seqlens, self.dA,
-                                                             self.ws_gemm)),
-            ("wgrad_down", lambda: L.moonep_wgrad(d, Hp, H, self.A, self.dZp, self.cu_seqlens, self.dW_down_home,
-                                                  sl(self.dW_down_slots), self.ws_wgrad)),
-            ("swiglu_backward", lambda: L.moonep_swiglu_backward(d, Hp, self.Ygu, self.dA, self.dYgu)),
+        dgrad_down = ("dgrad_down", lambda: L.moonep_group_gemm_dgrad(d, Hp, H, self.dZp, self.W_down_home,
+                                                                      sl(self.W_down_slots), self.cu_seqlens,
+                                                                      self.dA, self.ws_gemm))
+        wgrad_down = ("wgrad_down", lambda: L.moonep_wgrad(d, Hp, H, self.A, self.dZp, self.cu_seqlens,
+                                                           self.dW_down_home, sl(self.dW_down_slots),
+                                                           self.ws_wgrad))
+        if self.save8:
+            affine = (self.gamma, self.beta) if self.norm else (None, None)
+            calls = [
+                ("combine_backward", lambda: L.moonep_combine_backward_ungated(d, H, self.dout, self.dest_idx,
+                                                                               self.dZp)),
+                dgrad_down,
+                ("swiglu_backward8", lambda: L.moonep_swiglu_backward8(d, Hp, self.ygu_codes, self.ygu_exps, self.dA,
+                                                                       self.src_of_row, self.gates, self.A,
+                                                                       self.dYgu, self.dgates)),
+                wgrad_down,
+                ("dispatch8", lambda: L.moonep_dispatch8(d, H, self.x_codes, self.x_exps, *affine, self.dest_idx,
+                                                         self.Xp)),
+            ]
+        else:
+            calls = [
+                ("combine_backward", lambda: L.moonep_combine_backward(d, H, self.dout, self.Zp, self.dest_idx,
+                                                                       self.gates, self.dZp, self.dgates)),
+                dgrad_down,
+                wgrad_down,
+                ("swiglu_backward", lambda: L.moonep_swiglu_backward(d, Hp, self.Ygu, self.dA, self.dYgu)),
+            ]
+        calls += [
             ("dgrad_gate_up", lambda: L.moonep_group_gemm_dgrad(d, H, 2 * Hp, self.dYgu, self.W_gu_home,
                                                                 sl(self.W_gu_slots), self.cu_seqlens, self.dXp,
                                                                 self.ws_gemm)),
             ("wgrad_gate_up", lambda: L.moonep_wgrad(d, H, 2 * Hp, self.Xp, self.dYgu, self.cu_seqlens,
                                                      self.dW_gu_home, sl(self.dW_gu_slots), self.ws_wgrad)),
-            ("dispatch_backward", lambda: L.moonep_dispatch_backward(d, H, self.dXp, self.dest_idx, self.dX)),
+            ("dispatch_backward", lambda: L.moonep_dispatch_backward(d, H, self.dXp, self.dest_idx, self.dXn)),
             ("reduce_grad", lambda: (L.moonep_reduce_grad(d, H, 2 * Hp, sl(self.slot_expert), self.dW_gu_home,
                                                           sl(self.dW_gu_slots)),
                                      L.moonep_reduce_grad(d, Hp, H, sl(self.slot_expert), self.dW_down_home,
                                                           sl(self.dW_down_slots)))),
         ]
+        if self.norm and self.save8:
+            calls.append(("layernorm_backward", lambda: L.moonep_layernorm_backward8(
+                d, H, self.dXn, self.x_codes, self.x_exps, self.rstd, self.gamma, self.dX, self.dgamma, self.dbeta,
+                self.ws_norm)))
+        elif self.norm:
+            calls.append(("layernorm_backward", lambda: L.moonep_layernorm_backward(
+                d, H, self.dXn, self.X, self.mean, self.rstd, self.gamma, self.dX, self.dgamma, self.dbeta,
+                self.ws_norm)))
+        return calls
 
     def forward(self):
         for _, f in self.forward_calls():

@@ -1,0 +1,290 @@
+"""The gated expert FFN with a layer norm in front and 8-bit checkpoints, as one run (GPU).
+
+  * Inputs that 8 bits hold without loss (rows of +-1, so that the norm's rows are +-1; weights that select
+    one column, so that the activation's input stays on the 8-bit grid): the gradients are those of the FFN
+    that keeps everything, held to the float64 oracle within rel (1 + |ref|), rel = 1e-4 for float32 (as the
+    tiny float32 FFN).
+  * Ordinary bf16 inputs: the gradients against the FFN that keeps everything.  A kept value is off by at
+    most half a step, at most 1/128 of its block's largest magnitude (about 3 deviations at most of 32 normal
+    values), evenly spread: 0.29 steps rms, below 1.4% of a deviation.  A gradient has one such factor from the
+    rows and one from the activation, whose derivative multiplies it by at most about 2: within 5% of the
+    gradient's norm.
+  * Layers that share their row buffers, a pass captured in a graph and replayed, and calls whose outputs pass
+    256 MB: the same bits as without.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer as olayer
+from oracle import norm8
+from oracle import planner as oplanner
+from tests.gpu_util import DEV, assert_gemm_close, i32, np64, npi, rand_tensor, say
+from tests.plan_checks import random_routing
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def m():
+    import load_balanced_dispatch_amd as mod
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a visible GPU")
+    return mod
+
+
+def routed(L, seed, skew=1.5):
+    d = L.d
+    rng = np.random.default_rng(seed)
+    idx = random_routing(rng, d.R, d.S, d.K, d.E, skew)
+    gates = rng.dirichlet(np.ones(d.K), size=(d.R, d.S)).astype(np.float32)
+    L.topk_idx.copy_(torch.as_tensor(np.asarray(idx, dtype=np.int32)))
+    L.gates.copy_(torch.as_tensor(gates))
+    return np.asarray(idx), gates
+
+
+def grads(L):
+    names = ["out", "dgates", "dX", "dW_down_home", "dW_gu_home"] + (["dgamma", "dbeta"] if L.norm else [])
+    return {n: getattr(L, n).clone() for n in names}
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_lossless_checkpoints_against_the_oracle(m, norm):
+    R, E, B, S, K, H, Hp = 4, 16, 4, 32, 2, 128, 96
+    L = m.MoeFFN(R, E, B, S, K, H, Hp, dtype=F32, backward=True, norm=norm, eps=2.0 ** -30, save8=True)
+    idx, gates = routed(L, 21)
+    rng = np.random.default_rng(22)
+    # rows with as many +1 as -1: mean 0, variance 1, 1 / sqrt(1 + 2^-30) = 1 in float32
+    x = np.stack([rng.permutation(np.repeat([1.0, -1.0], H // 2)) for _ in range(R * S)]).reshape(R, S, H)
+    gamma, beta = rng.integers(8, 33, H) / 32.0, rng.integers(-16, 17, H) / 64.0
+    if not norm:
+        x = x * gamma + beta
+    pick = rng.integers(0, H, (E, 2 * Hp))
+    Wgu = np.zeros((E, H, 2 * Hp))
+    for e in range(E):
+        Wgu[e, pick[e], np.arange(2 * Hp)] = rng.choice([1.0, -1.0], 2 * Hp)
+    Wd = rng.standard_normal((E, Hp, H)) * Hp ** -0.5
+    dout = rng.standard_normal((R, S, H))
+    for t, v in ((L.X, x), (L.W_gu_home, Wgu), (L.W_down_home, Wd), (L.dout, dout)):
+        t.copy_(torch.as_tensor(v, dtype=F32))
+    if norm:
+        L.gamma.copy_(torch.as_tensor(gamma))
+        L.beta.copy_(torch.as_tensor(beta))
+    say("lossless checkpoints", "norm" if norm else "no norm")
+    L.forward()
+    L.backward()
+    torch.cuda.synchronize()
+    Wd, dout = np64(L.W_down_home), np64(L.dout)
+    g64 = gates.astype(np.float64)
+    z = x.reshape(-1, H)
+    rstd = np.ones(R * S)
+    xn = x
+    if norm:
+        y, _, rstd, z = norm8.layernorm(z, gamma, beta, 2.0 ** -30)
+        xn = y.reshape(R, S, H)
+    kept = norm8.load8(npi(L.ygu_codes).reshape(-1, Hp), npi(L.ygu_exps).reshape(-1, norm8.blocks(Hp)))
+    p = oplanner.plan(idx, E, B)
+    P = S * K
+    Xp = olayer.dispatch(xn, p.dest_idx)
+    Wgus, Wds = olayer.prefetch(Wgu, p.slot_expert), olayer.prefetch(Wd, p.slot_expert)
+    Ygu = olayer.group_gemm(Xp, Wgu, Wgus, p.cu_seqlens, P)
+    # the checkpoint holds what the oracle computes, to the norm's rounding: the case is lossless
+    assert np.abs(kept.reshape(Ygu.shape) - Ygu).max() < 1e-6
+    A = olayer.swiglu(Ygu)
+    Zp = olayer.group_gemm(A, Wd, Wds, p.cu_seqlens, P)
+    dZp, dgate = olayer.combine_backward(dout, Zp, p.dest_idx, g64)
+    dA = olayer.group_gemm_dgrad(dZp, Wd, Wds, p.cu_seqlens, P)
+    dYgu = olayer.swiglu_backward(Ygu, dA)
+    dXn = olayer.dispatch_backward(olayer.group_gemm_dgrad(dYgu, Wgu, Wgus, p.cu_seqlens, P), p.dest_idx)
+    dWd, dWds = np.zeros((E, Hp, H)), np.zeros((R, B, Hp, H))
+    dWgu, dWgus = np.zeros(Wgu.shape), np.zeros((R, B) + Wgu.shape[1:])
+    olayer.wgrad(A, dZp, p.cu_seqlens, P, dWd, dWds)
+    olayer.reduce_grad(p.slot_expert, dWd, dWds)
+    olayer.wgrad(Xp, dYgu, p.cu_seqlens, P, dWgu, dWgus)
+    olayer.reduce_grad(p.slot_expert, dWgu, dWgus)
+    assert_gemm_close(np64(L.out), olayer.combine(Zp, p.dest_idx, g64), 1e-4, "out")
+    assert_gemm_close(np64(L.dgates), dgate, 1e-4, "dgates")
+    assert_gemm_close(np64(L.dW_down_home), dWd, 1e-4, "dW_down")
+    assert_gemm_close(np64(L.dW_gu_home), dWgu, 1e-4, "dW_gate_up")
+    if norm:
+        dX, dgamma, dbeta = norm8.layernorm_backward(dXn.reshape(-1, H), z, rstd, gamma)
+        assert_gemm_close(np64(L.dX).reshape(-1, H), dX, 1e-4, "dX")
+        assert_gemm_close(np64(L.dgamma), dgamma, 1e-4, "dgamma")
+        assert_gemm_close(np64(L.dbeta), dbeta, 1e-4, "dbeta")
+    else:
+        assert_gemm_close(np64(L.dX), dXn, 1e-4, "dX")
+
+
+def fill(L, seed):
+    d, H, Hp = L.d, L.H, L.Hp
+    routed(L, seed)
+    L.X.copy_(rand_tensor((d.R, d.S, H), L.dtype, seed + 1))
+    L.W_gu_home.copy_(rand_tensor((d.E, H, 2 * Hp), L.dtype, seed + 2, std=H ** -0.5))
+    L.W_down_home.copy_(rand_tensor((d.E, Hp, H), L.dtype, seed + 3, std=Hp ** -0.5))
+    L.dout.copy_(rand_tensor((d.R, d.S, H), F32, seed + 4))
+    if L.norm:
+        L.gamma.copy_(1 + rand_tensor((H,), F32, seed + 5, std=0.2))
+        L.beta.copy_(rand_tensor((H,), F32, seed + 6, std=0.1))
+
+
+DIMS = (4, 16, 2, 128, 4, 256, 192)
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_checkpoints_against_keeping_everything(m, norm):
+    whole = m.MoeFFN(*DIMS, backward=True, norm=norm)
+    kept8 = m.MoeFFN(*DIMS, backward=True, norm=norm, save8=True)
+    for L in (whole, kept8):
+        fill(L, 31)
+        say("FFN", "save8" if L.save8 else "whole", "norm" if norm else "no norm")
+        L.forward()
+        L.backward()
+    torch.cuda.synchronize()
+    a, b = grads(whole), grads(kept8)
+    assert torch.equal(a["out"], b["out"])
+    for n in a:
+        off = float((a[n].double() - b[n].double()).norm() / a[n].double().norm())
+        assert off <= 0.05, (n, off)
+
+
+def test_norm_without_checkpoints_against_the_plain_ffn(m):
+    # the norm's own calls around an FFN that gets its rows from outside: the same bits
+    L = m.MoeFFN(*DIMS, backward=True, norm=True)
+    fill(L, 41)
+    L.forward()
+    L.backward()
+    plain = m.MoeFFN(*DIMS, backward=True)
+    fill(plain, 41)
+    plain.X.copy_(L.Xn)
+    plain.forward()
+    plain.backward()
+    torch.cuda.synchronize()
+    assert torch.equal(plain.out, L.out) and torch.equal(plain.dX, L.dXn)
+    assert torch.equal(plain.dW_gu_home, L.dW_gu_home) and torch.equal(plain.dgates, L.dgates)
+    dx, dg, db = norm8.layernorm_backward(np64(L.dXn).reshape(-1, L.H),
+                                          norm8.layernorm(np64(L.X).reshape(-1, L.H), np64(L.gamma), None, L.eps)[3],
+                                          np64(L.rstd).reshape(-1), np64(L.gamma))
+    assert_gemm_close(np64(L.dX).reshape(-1, L.H), dx, 1e-4, "dX")
+    assert_gemm_close(np64(L.dgamma), dg, 1e-4, "dgamma")
+    assert_gemm_close(np64(L.dbeta), db, 1e-4, "dbeta")
+
+
+def test_layers_share_their_row_buffers(m):
+    alone = [m.MoeFFN(*DIMS, backward=True, norm=True, save8=True) for _ in range(2)]
+    first = m.MoeFFN(*DIMS, backward=True, norm=True, save8=True)
+    shared = [first, m.MoeFFN(*DIMS, backward=True, norm=True, save8=True, scratch=first.scratch)]
+    for L, seed in zip(alone + shared, (51, 61, 51, 61)):
+        fill(L, seed)
+    say("shared row buffers")
+    for L in alone:
+        L.forward()
+        L.backward()
+    shared[0].forward()
+    shared[1].forward()   # overwrites the first layer's rows
+    shared[1].backward()
+    shared[0].backward()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, shared):
+        ga, gb = grads(a), grads(b)
+        assert all(torch.equal(ga[n], gb[n]) for n in ga)
+
+
+def test_captured_and_replayed(m):
+    L, E = (m.MoeFFN(*DIMS, backward=True, norm=True, save8=True) for _ in range(2))
+    sums = lambda x: [x.dW_gu_home, x.dW_down_home, x.dgamma, x.dbeta]  # noqa: E731
+
+    def step(x):
+        for t in sums(x):
+            t.zero_()
+        x.forward()
+        x.backward()
+
+    fill(L, 71)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(L)  # once before the capture, as torch asks
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(L)
+    for seed in (81, 91, 101, 81):
+        fill(L, seed)
+        fill(E, seed)
+        say("replay", seed)
+        g.replay()
+        step(E)  # the program's own eager work between the replays
+        torch.cuda.synchronize()
+        a, b = grads(L), grads(E)
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_outputs_past_256_mb_hold_the_same_bits(m):
+    # outputs this large are stored another way; halves of them are not
+    H, rows = 4096, 36000  # 295 MB of bf16
+    x = rand_tensor((rows, H), BF, 1)
+    gamma, beta = rand_tensor((H,), F32, 2), rand_tensor((H,), F32, 3)
+
+    def norm(x_):
+        n = x_.shape[0]
+        d = m.make_dims(1, 1, 0, n, 1)
+        Y = torch.empty_like(x_)
+        codes = torch.empty((n, H), dtype=torch.int8, device=DEV)
+        exps = torch.empty((n, H // 32), dtype=torch.uint8, device=DEV)
+        v = torch.empty_like(x_)
+        Xp = torch.empty_like(x_)
+        m.moonep_layernorm(d, H, x_, gamma, beta, 1e-5, Y, None, None, codes, exps)
+        m.moonep_load8(n, H, codes, exps, v)
+        dest = torch.arange(n, dtype=torch.int32, device=DEV)
+        m.moonep_dispatch8(d, H, codes, exps, gamma, beta, dest, Xp)
+        return Y, codes, exps, v, Xp
+
+    say("norm, load8, dispatch8 past 256 MB")
+    whole = norm(x)
+    cut = rows // 2
+    lo, hi = norm(x[:cut]), norm(x[cut:].clone())
+    for w, a, b in zip(whole, lo, hi):
+        assert torch.equal(w[:cut], a) and torch.equal(w[cut:], b)
+
+    def act(y, dA, rows_):
+        d = m.make_dims(1, 1, 0, rows_, 1)
+        A, A2, dY = torch.empty_like(dA), torch.empty_like(dA), torch.empty_like(y)
+        codes = torch.empty((rows_, 2, H), dtype=torch.int8, device=DEV)
+        exps = torch.empty((rows_, 2, H // 32), dtype=torch.uint8, device=DEV)
+        m.moonep_swiglu_save8(d, H, y, A, codes, exps)
+        m.moonep_swiglu_backward8(d, H, codes, exps, dA, None, None, A2, dY, None)
+        return A, codes, exps, A2, dY
+
+    y, dA = torch.cat([x, x.flip(0)], 1).contiguous(), x.flip(1).contiguous()
+    say("swiglu_save8, swiglu_backward8 past 256 MB")
+    whole = act(y, dA, rows)
+    lo, hi = act(y[:cut], dA[:cut], cut), act(y[cut:].clone(), dA[cut:].clone(), rows - cut)
+    for w, a, b in zip(whole, lo, hi):
+        assert torch.equal(w[:cut], a) and torch.equal(w[cut:], b)
+
+
+def test_infinities_and_nan_as_the_plain_activation(m):
+    # the checkpointing activation gives what moonep_swiglu gives, special values included
+    vals = torch.tensor([0.0, -0.0, 1e-30, -90.0, 90.0, -200.0, 200.0, 3e38, -3e38, float("inf"), float("-inf"),
+                         float("nan")], device=DEV)
+    g, u = torch.meshgrid(vals, vals, indexing="ij")
+    y = torch.cat([g.reshape(1, -1), u.reshape(1, -1)], 1).contiguous()
+    Hp = y.shape[1] // 2
+    d = m.make_dims(1, 1, 0, 1, 1)
+    a, b = torch.empty((1, Hp), device=DEV), torch.empty((1, Hp), device=DEV)
+    codes = torch.empty((1, 2, Hp), dtype=torch.int8, device=DEV)
+    exps = torch.empty((1, 2, m.moonep_save8_blocks(Hp)), dtype=torch.uint8, device=DEV)
+    m.moonep_swiglu(d, Hp, y, a)
+    m.moonep_swiglu_save8(d, Hp, y, b, codes, exps)
+    torch.cuda.synchronize()
+    x, z = np64(a), np64(b)
+    assert np.array_equal(np.isnan(x), np.isnan(z))
+    fine = np.isfinite(x) & np.isfinite(z)
+    assert np.array_equal(np.where(fine, 0, x), np.where(fine, 0, z), equal_nan=True)
+    # each side 16 u; sigmoid(-90) = 8e-40 is a denormal of 20 bits: half a step of it, 2^-150, times g times u on
+    # each side
+    gu = np64(y)[:, :Hp][fine] * np64(y)[:, Hp:][fine]
+    assert np.all(np.abs(x[fine] - z[fine]) <= 32 * 2.0 ** -24 * np.abs(x[fine]) + 4 * 2.0 ** -150 * np.abs(gu))
