@@ -335,6 +335,8 @@ def moonep_swiglu_backward(d: Dims, Hp: int, Ygu, dA, dYgu, stream=None):
 
 
 # ------------------------------------------------------------------ layer norm and 8-bit checkpoints
+import torch  # noqa: E402  (already loaded with the library)
+
 
 class _Call:
     """Checks the tensors of one call, which must all lie on one device, and makes it on that device's current
@@ -355,13 +357,15 @@ class _Call:
     def ptr(self, t, name, dtype, numel, optional=False):
         if t is None and optional:
             return None
-        p = _ptr(t, name, dtype, numel)
+        if not (t.__class__ is torch.Tensor and t.is_cuda and t.is_contiguous() and t.dtype is dtype
+                and t.numel() == numel):
+            _ptr(t, name, dtype, numel)  # says what is wrong (or that nothing is: a subclass, no dtype to hold to)
         device = t.get_device()
         if device != self.device:
             if self.device >= 0:
                 raise ValueError(f"{name} is on cuda:{device}, the tensors before it on cuda:{self.device}")
             self.device = device
-        return p
+        return t.data_ptr()
 
     def workspace(self, t, needed):
         p = self.ptr(t, "workspace", None, None)
@@ -370,7 +374,6 @@ class _Call:
         return p
 
     def __call__(self, entry, *args, stream=None):
-        import torch
         if stream is None:
             # the handle alone: torch.cuda.current_stream() costs 2-3 us, as much as a small kernel
             handle = torch._C._cuda_getCurrentRawStream(self.device)
@@ -392,7 +395,6 @@ def moonep_save8_blocks(C: int) -> int:
 
 def _codes(c, codes, exps, rows, C, optional=False):
     """Pointers of 8-bit rows [rows, C]."""
-    import torch
     return (c.ptr(codes, "codes", torch.int8, rows * C, optional),
             c.ptr(exps, "exps", torch.uint8, rows * moonep_save8_blocks(C), optional))
 
@@ -426,7 +428,6 @@ def moonep_swiglu_save8(d: Dims, Hp: int, Ygu, A, codes, exps, stream=None):
 def moonep_swiglu_backward8(d: Dims, Hp: int, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, stream=None):
     """Gradient of moonep_swiglu from its 8-bit input; with src_of_row, gates and dgates (all or none) the gates
     are applied here: A and dYgu come out times the gate, and dgates is <dA, silu(g) u> per pair."""
-    import torch
     c = _Call()
     N = d.N
     t, code = c.dtype(dA, "dA")
@@ -439,7 +440,6 @@ def moonep_swiglu_backward8(d: Dims, Hp: int, codes, exps, dA, src_of_row, gates
 
 def moonep_dispatch8(d: Dims, H: int, codes, exps, gamma, beta, dest_idx, Xp, stream=None):
     """moonep_dispatch from 8-bit token rows, times gamma plus beta (float32 [H], or None)."""
-    import torch
     c = _Call()
     t, code = c.dtype(Xp, "Xp")
     rows8 = _codes(c, codes, exps, d.R * d.S, H)
@@ -450,7 +450,6 @@ def moonep_dispatch8(d: Dims, H: int, codes, exps, gamma, beta, dest_idx, Xp, st
 
 def moonep_combine_backward_ungated(d: Dims, D: int, dout, dest_idx, dYp, stream=None):
     """The output gradient's rows laid out by expert, without gates."""
-    import torch
     c = _Call()
     t, code = c.dtype(dYp, "dYp")
     c(_LIB.moonep_combine_backward_ungated, d, int(D), code,
@@ -461,7 +460,6 @@ def moonep_combine_backward_ungated(d: Dims, D: int, dout, dest_idx, dYp, stream
 def moonep_layernorm(d: Dims, H: int, X, gamma, beta, eps: float, Y, mean, rstd, codes=None, exps=None, stream=None):
     """Layer norm of X [R,S,H]; mean and rstd [R,S] may be None, and codes and exps keep the normalised rows in
     8 bits."""
-    import torch
     c = _Call()
     t, code = c.dtype(X, "X")
     T, f32 = d.R * d.S, torch.float32
@@ -476,7 +474,6 @@ def moonep_layernorm_backward_workspace_bytes(d: Dims, H: int) -> int:
 
 
 def _layernorm_backward(c, entry, d, H, dtype, dY, z, rstd, gamma, dX, dgamma, dbeta, workspace, stream):
-    import torch
     T, f32 = d.R * d.S, torch.float32
     c(entry, d, int(H), *dtype, c.ptr(dY, "dY", f32, T * H), *z, c.ptr(rstd, "rstd", f32, T),
       c.ptr(gamma, "gamma", f32, H), c.ptr(dX, "dX", f32, T * H), c.ptr(dgamma, "dgamma", f32, H),
@@ -486,7 +483,6 @@ def _layernorm_backward(c, entry, d, H, dtype, dY, z, rstd, gamma, dX, dgamma, d
 
 def moonep_layernorm_backward(d: Dims, H: int, dY, X, mean, rstd, gamma, dX, dgamma, dbeta, workspace, stream=None):
     """Gradients of moonep_layernorm from its input: writes dX, adds into dgamma and dbeta (or None)."""
-    import torch
     c = _Call()
     t, code = c.dtype(X, "X")
     T = d.R * d.S

@@ -365,6 +365,107 @@ __global__ __launch_bounds__(MAXT) void layernorm_bwd_rows(const float* __restri
   }
 }
 
+// Few rows: one launch and no partial sums.  Blocks [0, row_blocks) take the rows, a wave (ROW_WAVE) or a
+// block each, and read them twice, for the means and for dX; the others take 64 columns each over all rows, dealt to
+// their 64 groups of 16 lanes, for dgamma and dbeta.  The second and third reads come from the caches.
+constexpr int kFewThreads = 1024;
+constexpr int kFewCols = 64;   // columns of a column block
+constexpr int kFewBatch = 4;   // rows a group of its lanes loads together
+
+template <typename Z, bool AL, bool ROW_WAVE>
+__global__ __launch_bounds__(kFewThreads) void layernorm_bwd_few(const float* __restrict__ dY, Z src,
+                                                                 const float* __restrict__ rstd,
+                                                                 const float* __restrict__ gamma,
+                                                                 float* __restrict__ dX, float* __restrict__ dgamma,
+                                                                 float* __restrict__ dbeta, int rows, int H,
+                                                                 int row_blocks) {
+  constexpr int kWaves = kFewThreads / 64;
+  __shared__ union {
+    float sums[2][kWaves];
+    f32x4 fold[kWaves][2][16];
+  } lds;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  if ((int)blockIdx.x < row_blocks) {
+    const int64_t row = ROW_WAVE ? (int64_t)blockIdx.x * kWaves + wv : blockIdx.x;
+    if (row >= rows) return;  // with ROW_WAVE only, which has no barrier
+    const int t = ROW_WAVE ? lane : threadIdx.x, lanes = ROW_WAVE ? 64 : kFewThreads;
+    const float r = rstd[row];
+    const typename Z::Row q = src.row(row);
+    float s1 = 0.f, s2 = 0.f;
+    for (int col = t * kQuad; col < H; col += lanes * kQuad) {
+      const f32x4 dy = load4<AL>(dY + row * H, col, H), w = load4<AL>(gamma, col, H);
+      const f32x4 z = src.z(src.load(row, col, H), q, r);
+#pragma unroll
+      for (int i = 0; i < kQuad; ++i) {
+        const float gy = dy[i] * w[i];
+        s1 += gy;
+        if (AL || col + i < H) s2 = __builtin_fmaf(gy, z[i], s2);
+      }
+    }
+    s1 = row_sum<ROW_WAVE>(s1, lds.sums[0]) / (float)H;
+    s2 = row_sum<ROW_WAVE>(s2, lds.sums[1]) / (float)H;
+    for (int col = t * kQuad; col < H; col += lanes * kQuad) {
+      const f32x4 dy = load4<AL>(dY + row * H, col, H), w = load4<AL>(gamma, col, H);
+      const f32x4 z = src.z(src.load(row, col, H), q, r);
+      f32x4 dx;
+#pragma unroll
+      for (int i = 0; i < kQuad; ++i) dx[i] = r * (__builtin_fmaf(dy[i], w[i], -s1) - z[i] * s2);
+      store4<AL>(dX + row * H, col, H, dx);
+    }
+    return;
+  }
+  constexpr int kGroups = kFewThreads / 16;
+  const int group = threadIdx.x >> 4, col = ((int)blockIdx.x - row_blocks) * kFewCols + (lane & 15) * kQuad;
+  f32x4 dg = (f32x4)(0.f), db = (f32x4)(0.f);
+  for (int r0 = group; r0 < rows; r0 += kGroups * kFewBatch) {
+    f32x4 dy[kFewBatch];
+    typename Z::Chunk c[kFewBatch];
+    typename Z::Row q[kFewBatch];
+    float r[kFewBatch];
+#pragma unroll
+    for (int k = 0; k < kFewBatch; ++k) {
+      const int64_t row = min(r0 + k * kGroups, rows - 1);
+      dy[k] = load4<AL>(dY + row * H, col, H);
+      c[k] = src.load(row, col, H);
+      q[k] = src.row(row);
+      r[k] = rstd[row];
+    }
+#pragma unroll
+    for (int k = 0; k < kFewBatch; ++k) {
+      if (r0 + k * kGroups >= rows) break;
+      const f32x4 z = src.z(c[k], q[k], r[k]);
+#pragma unroll
+      for (int i = 0; i < kQuad; ++i) {
+        dg[i] = __builtin_fmaf(dy[k][i], z[i], dg[i]);
+        db[i] += dy[k][i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kQuad; ++i) {  // the wave's four groups
+    dg[i] += __shfl_xor(dg[i], 16, 64);
+    db[i] += __shfl_xor(db[i], 16, 64);
+    dg[i] += __shfl_xor(dg[i], 32, 64);
+    db[i] += __shfl_xor(db[i], 32, 64);
+  }
+  if (lane < 16) {
+    lds.fold[wv][0][lane] = dg;
+    lds.fold[wv][1][lane] = db;
+  }
+  __syncthreads();
+  const int k = threadIdx.x >> 4;  // 0: dgamma, 1: dbeta
+  if (k < 2 && (k == 0 || dbeta != nullptr)) {
+    float* out = k ? dbeta : dgamma;
+    f32x4 v = lds.fold[0][k][lane & 15];
+    for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+      for (int i = 0; i < kQuad; ++i) v[i] += lds.fold[w][k][lane & 15][i];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i)
+      if (col + i < H) out[col + i] += v[i];
+  }
+}
+
 // dgamma += the sum of the blocks' parts, and dbeta: 64 columns to a block, the parts dealt to its
 // 16 waves and their sums added in order.
 constexpr int kFoldWaves = 16;
@@ -471,9 +572,32 @@ void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, con
 #undef MOONEP_LN
 }
 
+// Up to this many rows the one launch is faster at every width (512 rows, measured on the GPU alone: 4.8 us
+// against 6.6 at 128 columns, 7.7 against 10.0 at 2048, 14.6 against 15.6 at 7168; 256 rows of 2048: 5.5
+// against 9.0); with 1024 rows the two are at 1024 columns and more (10.1 us against 11.3, 20.5 against 26.0 at 7168).
+constexpr int kFewRows = 512;
+// Widths to which a wave per row is faster there than a block (256 rows: 6.5 us against 7.5 at 1024 columns, but 4.7
+// against 3.5 for 16 rows).
+constexpr int kFewWaveWidth = 512;
+
+// Both launches of the backward: the rows, which leave partial sums, and their folding; or the one for few rows.
 template <typename Z, bool AL>
-void layernorm_bwd_launch(const RowShape& q, unsigned grid, int64_t rows, int H, const float* dY, Z z,
-                          const float* rstd, const float* gamma, float* dX, float* part, hipStream_t s) {
+void layernorm_bwd_launch(int64_t rows, int H, const float* dY, Z z, const float* rstd, const float* gamma, float* dX,
+                          float* dgamma, float* dbeta, float* part, hipStream_t s) {
+  if (rows <= kFewRows) {
+    const bool wave = H <= kFewWaveWidth;
+    const int row_blocks = wave ? (int)ceil_div_u(rows, kFewThreads / 64) : (int)rows;
+    const dim3 grid(row_blocks + ceil_div_u(H, kFewCols)), block(kFewThreads);
+    if (wave)
+      hipLaunchKernelGGL((layernorm_bwd_few<Z, AL, true>), grid, block, 0, s, dY, z, rstd, gamma, dX, dgamma, dbeta,
+                         (int)rows, H, row_blocks);
+    else
+      hipLaunchKernelGGL((layernorm_bwd_few<Z, AL, false>), grid, block, 0, s, dY, z, rstd, gamma, dX, dgamma, dbeta,
+                         (int)rows, H, row_blocks);
+    return;
+  }
+  const RowShape q = bwd_shape(H);
+  const unsigned grid = bwd_blocks(rows, q);
   const dim3 block(q.lanes == 64 ? 256 : q.lanes);
 #define MOONEP_LNB(NC, MAXT, AHEAD)                                                                                \
   hipLaunchKernelGGL((layernorm_bwd_rows<Z, AL, NC, MAXT, AHEAD>), dim3(grid), block, 0, s, dY, z, rstd, gamma, dX, part, \
@@ -491,6 +615,8 @@ void layernorm_bwd_launch(const RowShape& q, unsigned grid, int64_t rows, int H,
     MOONEP_LNB(8, 1024, false);
   }
 #undef MOONEP_LNB
+  hipLaunchKernelGGL(layernorm_fold, dim3(ceil_div_u(H, 64), dbeta ? 2 : 1), dim3(kFoldWaves * 64), 0, s, part,
+                     (int)grid, H, dgamma, dbeta);
 }
 
 int check_width(const char* name, int32_t H) {
@@ -501,23 +627,6 @@ int check_width(const char* name, int32_t H) {
 int bwd_checks(const char* name, const moonep_dims& d, int32_t H) {
   if (int rc = check_dims(d, name)) return rc;
   return check_width(name, H);
-}
-
-// The checks and the launches that both backward entries share; `go` launches the row kernel.
-template <typename F>
-int bwd_entry(const char* name, const moonep_dims& d, int32_t H, float* dgamma, float* dbeta, void* workspace,
-              hipStream_t s, F go) {
-  const int64_t rows = (int64_t)d.R * d.S;
-  const RowShape q = bwd_shape(H);
-  const unsigned grid = bwd_blocks(rows, q);
-  float* part = static_cast<float*>(workspace);
-  clear_stale_error();
-  go(q, grid, rows, part);
-  MOONEP_LAUNCH_CHECK(name);
-  hipLaunchKernelGGL(layernorm_fold, dim3(ceil_div_u(H, 64), dbeta ? 2 : 1), dim3(kFoldWaves * 64), 0, s, part,
-                     (int)grid, H, dgamma, dbeta);
-  MOONEP_LAUNCH_CHECK(name);
-  return MOONEP_OK;
 }
 
 }  // namespace
@@ -574,18 +683,22 @@ extern "C" int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype 
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
   const bool al = H % kQuad == 0 && aligned_to(X, t == MOONEP_BF16 ? 8 : 16) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
-  return bwd_entry(name, d, H, dgamma, dbeta, workspace, s,
-                   [&](const RowShape& q, unsigned grid, int64_t rows, float* part) {
-                     if (t == MOONEP_BF16) {
-                       const uint16_t* x = static_cast<const uint16_t*>(X);
-                       if (al) layernorm_bwd_launch<ZFromBf16<true>, true>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
-                       else layernorm_bwd_launch<ZFromBf16<false>, false>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
-                     } else {
-                       const float* x = static_cast<const float*>(X);
-                       if (al) layernorm_bwd_launch<ZFromF32<true>, true>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
-                       else layernorm_bwd_launch<ZFromF32<false>, false>(q, grid, rows, H, dY, {x, mean}, rstd, gamma, dX, part, s);
-                     }
-                   });
+  const int64_t rows = (int64_t)d.R * d.S;
+  float* part = static_cast<float*>(workspace);
+  clear_stale_error();
+#define MOONEP_LNB(T, ZFrom, AL)                                                                                   \
+  layernorm_bwd_launch<ZFrom<AL>, AL>(rows, H, dY, {static_cast<const T*>(X), mean}, rstd, gamma, dX, dgamma, dbeta, \
+                                      part, s)
+  if (t == MOONEP_BF16) {
+    if (al) MOONEP_LNB(uint16_t, ZFromBf16, true);
+    else MOONEP_LNB(uint16_t, ZFromBf16, false);
+  } else {
+    if (al) MOONEP_LNB(float, ZFromF32, true);
+    else MOONEP_LNB(float, ZFromF32, false);
+  }
+#undef MOONEP_LNB
+  MOONEP_LAUNCH_CHECK(name);
+  return MOONEP_OK;
 }
 
 extern "C" int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float* dY, const int8_t* codes,
@@ -598,9 +711,13 @@ extern "C" int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float*
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
   const bool al = H % kQuad == 0 && aligned_to(codes, 4) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
-  return bwd_entry(name, d, H, dgamma, dbeta, workspace, s,
-                   [&](const RowShape& q, unsigned grid, int64_t rows, float* part) {
-                     if (al) layernorm_bwd_launch<ZFrom8<true>, true>(q, grid, rows, H, dY, {codes, exps}, rstd, gamma, dX, part, s);
-                     else layernorm_bwd_launch<ZFrom8<false>, false>(q, grid, rows, H, dY, {codes, exps}, rstd, gamma, dX, part, s);
-                   });
+  const int64_t rows = (int64_t)d.R * d.S;
+  float* part = static_cast<float*>(workspace);
+  clear_stale_error();
+  if (al)
+    layernorm_bwd_launch<ZFrom8<true>, true>(rows, H, dY, {codes, exps}, rstd, gamma, dX, dgamma, dbeta, part, s);
+  else
+    layernorm_bwd_launch<ZFrom8<false>, false>(rows, H, dY, {codes, exps}, rstd, gamma, dX, dgamma, dbeta, part, s);
+  MOONEP_LAUNCH_CHECK(name);
+  return MOONEP_OK;
 }

@@ -350,7 +350,24 @@ def test_layernorm_checkpoint_is_save8_of_its_rows(m, H):
 @pytest.mark.parametrize("dtype", [BF, F32, "8"])
 @pytest.mark.parametrize("H", NORM_WIDTHS)
 def test_layernorm_backward(m, dtype, H):
-    R, S = 3, 7 if H > 4096 else 43
+    # few rows: one launch
+    backward_case(m, dtype, H, 3, 7 if H > 4096 else 43)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32, "8"])
+@pytest.mark.parametrize("H", [1, 7, 64, 253, 512, 1000, 1024, 1413, 2048, 2500, 7168, 8192, 16384, 20001, 32768])
+def test_layernorm_backward_more_rows(m, dtype, H):
+    # more than 512 rows: the rows' blocks leave partial sums, a second launch folds them
+    backward_case(m, dtype, H, 3, 173)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 63, 64, 65, 256, 257, 511, 512, 513])
+@pytest.mark.parametrize("H", [72, 520])
+def test_layernorm_backward_row_counts(m, rows, H):
+    backward_case(m, BF, H, 1, rows)
+
+
+def backward_case(m, dtype, H, R, S):
     rows = R * S
     d = m.make_dims(R, R, 0, S, 1)
     x = norm_rows(rows, H, F32 if dtype == "8" else dtype, H)
