@@ -22,24 +22,31 @@
 namespace moonep {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr unsigned kMaxBlocks = 1u << 22;  // a launch counts its threads in 32 bits; more work than that is looped over
+// Threads to a block.  Aligned rows run fastest in blocks of one wave, which start and end by themselves: the
+// activation with its checkpoint read back, 196 608 x 1408, 637 us (643 with 128 threads, 668 with 256, 646 with
+// 512), its backward, 262 144 x 2048, 901 us (909, 938).  Rows off their alignment run fastest in large ones, whose
+// waves share the lines at the ends of their pieces in one L1: 32 768 x 1413, 160 us (168 with 256, 181 with 128).
+constexpr int stream_threads(bool al) { return al ? 64 : 512; }
+constexpr int bwd8_threads(bool al) { return al ? 64 : 256; }
+constexpr int kScatterThreads = 128;  // 262 144 x 7168 rows of an output gradient: 852 us, 857 with 64, 884 with 256
 
-constexpr int kMaxWidth = 1 << 30;         // column numbers stay clear of 32 bits
+constexpr int64_t kMaxThreads = 1 << 30;  // a launch counts its threads in 32 bits; more work than that is looped over
+constexpr int kMaxWidth = 1 << 30;        // column numbers stay clear of 32 bits
 
-unsigned grid_for(int64_t threads) {
-  const int64_t b = (threads + kThreads - 1) / kThreads;
-  return (unsigned)(b < (int64_t)kMaxBlocks ? b : (int64_t)kMaxBlocks);
+unsigned grid_for(int64_t threads, int block) {
+  const int64_t t = threads < kMaxThreads ? threads : kMaxThreads;
+  return (unsigned)((t + block - 1) / block);
 }
 
 // ------------------------------------------------------------------ rows
 
 template <typename T, bool AL>
-__global__ __launch_bounds__(kThreads) void save8_rows(const T* __restrict__ X, int8_t* __restrict__ codes,
+__global__ __launch_bounds__(stream_threads(AL)) void save8_rows(const T* __restrict__ X, int8_t* __restrict__ codes,
                                                        uint8_t* __restrict__ exps, int64_t rows, int C) {
+  constexpr int kT = stream_threads(AL);
   const int nb = (C + kBlock8 - 1) / kBlock8;
   const int64_t total = rows * nb * 4;  // whole quads
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x; i < total; i += (int64_t)gridDim.x * kT) {
     const int64_t blk = i >> 2, row = blk / nb;
     const int col = (int)(blk - row * nb) * kBlock8 + (int)(i & 3) * kChunk;
     float f[kChunk];
@@ -51,12 +58,13 @@ __global__ __launch_bounds__(kThreads) void save8_rows(const T* __restrict__ X, 
 }
 
 template <typename T, bool AL, bool PAST>
-__global__ __launch_bounds__(kThreads) void load8_rows(const int8_t* __restrict__ codes,
+__global__ __launch_bounds__(stream_threads(AL)) void load8_rows(const int8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ exps, T* __restrict__ X,
                                                        int64_t rows, int C) {
+  constexpr int kT = stream_threads(AL);
   const int nb = (C + kBlock8 - 1) / kBlock8, nc = chunks8(C);
   const int64_t total = rows * nc;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x; i < total; i += (int64_t)gridDim.x * kT) {
     const int64_t row = i / nc;
     const int c = (int)(i - row * nc), col = c * kChunk;
     float f[kChunk];
@@ -92,12 +100,13 @@ __device__ __forceinline__ float sigmoid_f(float g) {
 }
 
 template <typename T, bool AL, bool PAST>
-__global__ __launch_bounds__(kThreads) void swiglu_save8_rows(const T* __restrict__ Ygu, T* __restrict__ A,
+__global__ __launch_bounds__(stream_threads(AL)) void swiglu_save8_rows(const T* __restrict__ Ygu, T* __restrict__ A,
                                                               int8_t* __restrict__ codes, uint8_t* __restrict__ exps,
                                                               int64_t rows, int Hp) {
+  constexpr int kT = stream_threads(AL);
   const int nb = (Hp + kBlock8 - 1) / kBlock8;
   const int64_t total = rows * nb * 4;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x; i < total; i += (int64_t)gridDim.x * kT) {
     const int64_t blk = i >> 2, row = blk / nb;
     const int j = (int)(blk - row * nb), col = j * kBlock8 + (int)(i & 3) * kChunk;
     float g[kChunk], u[kChunk], a[kChunk];
@@ -126,17 +135,18 @@ __device__ __forceinline__ float wave_sum_f(float x) {
 // The gate's gradient is a chain per lane and a fixed butterfly across the wave, so it does not depend on
 // timing.
 template <typename T, bool AL, bool PAST, int NC>
-__global__ __launch_bounds__(kThreads) void swiglu_bwd8_rows(const int8_t* __restrict__ codes,
+__global__ __launch_bounds__(bwd8_threads(AL)) void swiglu_bwd8_rows(const int8_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ exps,
                                                              const T* __restrict__ dA,
                                                              const int32_t* __restrict__ src_of_row,
                                                              const float* __restrict__ gates, T* __restrict__ A,
                                                              T* __restrict__ dYgu, float* __restrict__ dgates,
                                                              int64_t rows, int Hp) {
+  constexpr int kT = bwd8_threads(AL);
   const int lane = threadIdx.x & 63;
   const int nb = (Hp + kBlock8 - 1) / kBlock8, nc = chunks8(Hp);
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); row < rows; row += step) {
+  const int64_t step = (int64_t)gridDim.x * (kT / 64);
+  for (int64_t row = (int64_t)blockIdx.x * (kT / 64) + (threadIdx.x >> 6); row < rows; row += step) {
     const int8_t* cr = codes + row * 2 * Hp;
     const uint8_t* er = exps + row * 2 * nb;
     float dot = 0.f, w = 1.f;
@@ -228,11 +238,12 @@ struct FromF32 {
 // One wave per 64 chunks of a token's row, read once and stored K times (rows with destination -1 are
 // left out), as the bf16 dispatch does.
 template <typename T, bool AL, bool PAST, typename Src>
-__global__ __launch_bounds__(kThreads) void scatter_rows(Src src, const int32_t* __restrict__ dest,
+__global__ __launch_bounds__(kScatterThreads) void scatter_rows(Src src, const int32_t* __restrict__ dest,
                                                          T* __restrict__ Xp, int64_t tokens, int K, int C,
                                                          int pieces) {
-  const int64_t waves = tokens * pieces, step = (int64_t)gridDim.x * (kThreads / 64);
-  for (int64_t g = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); g < waves; g += step) {
+  constexpr int kT = kScatterThreads;
+  const int64_t waves = tokens * pieces, step = (int64_t)gridDim.x * (kT / 64);
+  for (int64_t g = (int64_t)blockIdx.x * (kT / 64) + (threadIdx.x >> 6); g < waves; g += step) {
     const int64_t tok = g / pieces;
     const int col = ((int)(g - tok * pieces) * 64 + (int)(threadIdx.x & 63)) * kChunk;
     if (col >= C) continue;
@@ -250,9 +261,9 @@ template <typename T, template <bool> class Src, typename... Args>
 void scatter_launch(bool al, const int32_t* dest, void* Xp, const moonep_dims& d, int C, hipStream_t s, Args... args) {
   const int64_t tokens = (int64_t)d.R * d.S;
   const int pieces = (chunks8(C) + 63) / 64;
-  const unsigned grid = grid_for(tokens * pieces * 64);
+  const unsigned grid = grid_for(tokens * pieces * 64, kScatterThreads);
 #define MOONEP_SCATTER(AL, PAST)                                                                        \
-  hipLaunchKernelGGL((scatter_rows<T, AL, PAST, Src<AL>>), dim3(grid), dim3(kThreads), 0, s, Src<AL>{args...}, dest, \
+  hipLaunchKernelGGL((scatter_rows<T, AL, PAST, Src<AL>>), dim3(grid), dim3(kScatterThreads), 0, s, Src<AL>{args...}, dest, \
                      static_cast<T*>(Xp), tokens, d.K, C, pieces)
   MOONEP_BY_ROWS(T, al, n_pairs(d) * C * (int64_t)sizeof(T), MOONEP_SCATTER);
 #undef MOONEP_SCATTER
@@ -265,15 +276,15 @@ int rows_launch(const char* name, bool save, int64_t rows, int C, const void* X,
   int8_t* c = const_cast<int8_t*>(static_cast<const int8_t*>(codes));
   uint8_t* e = const_cast<uint8_t*>(static_cast<const uint8_t*>(exps));
   if (save) {
-    const unsigned grid = grid_for(rows * blocks8(C) * 4);
+    const dim3 grid(grid_for(rows * blocks8(C) * 4, stream_threads(al))), block(stream_threads(al));
     const T* x = static_cast<const T*>(X);
-    if (al) hipLaunchKernelGGL((save8_rows<T, true>), dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, C);
-    else hipLaunchKernelGGL((save8_rows<T, false>), dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, C);
+    if (al) hipLaunchKernelGGL((save8_rows<T, true>), grid, block, 0, s, x, c, e, rows, C);
+    else hipLaunchKernelGGL((save8_rows<T, false>), grid, block, 0, s, x, c, e, rows, C);
   } else {
-    const unsigned grid = grid_for(rows * chunks8(C));
+    const dim3 grid(grid_for(rows * chunks8(C), stream_threads(al))), block(stream_threads(al));
     T* x = static_cast<T*>(Xout);
 #define MOONEP_LOAD8(AL, PAST) \
-  hipLaunchKernelGGL((load8_rows<T, AL, PAST>), dim3(grid), dim3(kThreads), 0, s, c, e, x, rows, C)
+  hipLaunchKernelGGL((load8_rows<T, AL, PAST>), grid, block, 0, s, c, e, x, rows, C)
     MOONEP_BY_ROWS(T, al, rows * C * (int64_t)sizeof(T), MOONEP_LOAD8);
 #undef MOONEP_LOAD8
   }
@@ -305,12 +316,12 @@ int rows_entry(const char* name, bool save, int64_t rows, int32_t C, moonep_dtyp
 
 template <typename T>
 int swiglu_save8_launch(int64_t rows, int Hp, const void* Ygu, void* A, int8_t* codes, uint8_t* exps, hipStream_t s) {
-  const unsigned grid = grid_for(rows * blocks8(Hp) * 4);
   const T* y = static_cast<const T*>(Ygu);
   T* a = static_cast<T*>(A);
   const bool al = Hp % kChunk == 0 && aligned16(Ygu) && aligned16(A) && aligned_to(codes, 8);
+  const dim3 grid(grid_for(rows * blocks8(Hp) * 4, stream_threads(al))), block(stream_threads(al));
 #define MOONEP_SAVE8(AL, PAST) \
-  hipLaunchKernelGGL((swiglu_save8_rows<T, AL, PAST>), dim3(grid), dim3(kThreads), 0, s, y, a, codes, exps, rows, Hp)
+  hipLaunchKernelGGL((swiglu_save8_rows<T, AL, PAST>), grid, block, 0, s, y, a, codes, exps, rows, Hp)
   MOONEP_BY_ROWS(T, al, rows * Hp * (int64_t)sizeof(T), MOONEP_SAVE8);
 #undef MOONEP_SAVE8
   MOONEP_LAUNCH_CHECK("moonep_swiglu_save8");
@@ -322,16 +333,17 @@ int swiglu_bwd8_launch(int64_t rows, int Hp, const int8_t* codes, const uint8_t*
                        const int32_t* src_of_row, const float* gates, void* A, void* dYgu, float* dgates,
                        hipStream_t s) {
   const bool al = Hp % kChunk == 0 && aligned16(dA) && aligned16(A) && aligned16(dYgu) && aligned_to(codes, 8);
-  const int nc = al ? (chunks8(Hp) + 63) / 64 : 1;
+  const int nc = (chunks8(Hp) + 63) / 64;
+  const dim3 grid(grid_for(rows * 64, bwd8_threads(al))), block(bwd8_threads(al));
 #define MOONEP_BWD8_NC(AL, PAST, NC)                                                                                 \
-  hipLaunchKernelGGL((swiglu_bwd8_rows<T, AL, PAST, NC>), dim3(grid_for(rows * 64)), dim3(kThreads), 0, s, codes, exps, \
+  hipLaunchKernelGGL((swiglu_bwd8_rows<T, AL, PAST, NC>), grid, block, 0, s, codes, exps, \
                      static_cast<const T*>(dA), src_of_row, gates, static_cast<T*>(A), static_cast<T*>(dYgu), dgates, \
                      rows, Hp)
-#define MOONEP_BWD8(AL, PAST)                       \
-  if (!(AL) || nc == 1) MOONEP_BWD8_NC(AL, PAST, 1); \
-  else if (nc == 2) MOONEP_BWD8_NC(AL, PAST, AL ? 2 : 1); \
-  else if (nc == 3) MOONEP_BWD8_NC(AL, PAST, AL ? 3 : 1); \
-  else MOONEP_BWD8_NC(AL, PAST, AL ? 4 : 1)
+#define MOONEP_BWD8(AL, PAST)                 \
+  if (nc == 1) MOONEP_BWD8_NC(AL, PAST, 1);   \
+  else if (nc == 2) MOONEP_BWD8_NC(AL, PAST, 2); \
+  else if (nc == 3) MOONEP_BWD8_NC(AL, PAST, 3); \
+  else MOONEP_BWD8_NC(AL, PAST, 4)
   MOONEP_BY_ROWS(T, al, rows * Hp * (int64_t)sizeof(T), MOONEP_BWD8);
 #undef MOONEP_BWD8
 #undef MOONEP_BWD8_NC
