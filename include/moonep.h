@@ -345,8 +345,8 @@ int moonep_load8(int64_t rows, int32_t C, moonep_dtype t, const int8_t* codes, c
                  moonep_stream stream);
 
 /*
- * moonep_swiglu_save8 -- moonep_swiglu, and its input kept in 8 bits in the same pass.  Each row's gate and
- *   up halves are coded as rows of their own: the codes are those of moonep_save8 of Ygu as [2*R*S*K, Hp].
+ * moonep_swiglu_save8 -- moonep_swiglu (the same A, bit for bit), and its input kept in 8 bits in the same pass.  Each
+ *   row's gate and up halves are coded as rows of their own: the codes are those of moonep_save8 of Ygu as [2*R*S*K, Hp].
  * In:  Ygu [R*S*K, 2*Hp] dtype t.
  * Out: A [R*S*K, Hp] dtype t;  codes [R*S*K, 2, Hp] int8;  exps [R*S*K, 2, moonep_save8_blocks(Hp)] uint8.
  */
@@ -419,7 +419,7 @@ size_t moonep_layernorm_backward_workspace_bytes(moonep_dims d, int32_t H);
  *      codes and exps;  rstd [R,S], gamma [H] float32.
  * Out: dX [R,S,H] float32.   In/Out: dgamma, dbeta [H] float32 (dbeta NULL to skip).
  * workspace: moonep_layernorm_backward_workspace_bytes(d, H) bytes of device memory (256-byte aligned), contents
- * ignored on entry.
+ * ignored on entry; calls that can overlap (two streams, two replayed graphs) need one each.
  */
 int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype t, const float* dY, const void* X,
                               const float* mean, const float* rstd, const float* gamma, float* dX, float* dgamma,

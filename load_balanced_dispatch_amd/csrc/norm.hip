@@ -680,6 +680,7 @@ extern "C" int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype 
   MOONEP_REQUIRE(aligned_to(X, elem_bytes(t)), "%s: a row pointer is not aligned to its elements", name);
   if ((int64_t)d.R * d.S == 0) return MOONEP_OK;
   MOONEP_REQUIRE(dY && X && mean && rstd && gamma && dX && dgamma && workspace, "%s: null pointer", name);
+  MOONEP_REQUIRE(aligned_to(dY, 4) && aligned_to(dX, 4), "%s: a row pointer is not aligned to its elements", name);
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
   const bool al = H % kQuad == 0 && aligned_to(X, t == MOONEP_BF16 ? 8 : 16) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
@@ -708,6 +709,7 @@ extern "C" int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float*
   if (int rc = bwd_checks(name, d, H)) return rc;
   if ((int64_t)d.R * d.S == 0) return MOONEP_OK;
   MOONEP_REQUIRE(dY && codes && exps && rstd && gamma && dX && dgamma && workspace, "%s: null pointer", name);
+  MOONEP_REQUIRE(aligned_to(dY, 4) && aligned_to(dX, 4), "%s: a row pointer is not aligned to its elements", name);
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
   const bool al = H % kQuad == 0 && aligned_to(codes, 4) && aligned16(dY) && aligned16(dX) && aligned16(gamma);

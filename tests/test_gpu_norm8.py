@@ -121,6 +121,26 @@ def test_save8_extremes(m):
     assert ref[6, :5].tolist() == [-127.0, 127.0, 126.0, 126.0, 64.0]
 
 
+def test_denormal_blocks_in_bf16(m):
+    # bf16 rows whose blocks reach below 2^-126: the codes, and the values written back as bf16 and float32
+    x = (torch.arange(-32, 32, device=DEV).float() * 2.0 ** -131).to(BF).reshape(1, 64)
+    x[0, 40] = 1.5 * 2.0 ** -127
+    codes = torch.empty((1, 64), dtype=torch.int8, device=DEV)
+    exps = torch.empty((1, 2), dtype=torch.uint8, device=DEV)
+    m.moonep_save8(1, 64, x, codes, exps)
+    rc, re = norm8.save8(np64(x))
+    for out in (BF, F32):
+        v = torch.empty((1, 64), dtype=out, device=DEV)
+        m.moonep_load8(1, 64, codes, exps, v)
+        torch.cuda.synchronize()
+        # read as bits: the host may flush denormals in a conversion
+        bits = v.view(torch.int16 if out == BF else torch.int32).cpu().numpy().astype(np.int64) & 0xFFFFFFFF
+        got = (bits & 0xFFFF) << 16 if out == BF else bits
+        got = got.astype(np.uint32).view(np.float32).astype(np.float64)
+        assert np.array_equal(got, norm8.load8(rc, re))
+    assert np.array_equal(npi(exps), re) and np.array_equal(npi(codes), rc)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("Hp", [1, 13, 32, 253, 256, 1408, 2048])
 def test_swiglu_save8(m, dtype, Hp):

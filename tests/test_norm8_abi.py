@@ -79,7 +79,9 @@ def test_arguments_that_go_together():
 @pytest.mark.parametrize("name,which", [("moonep_save8", 0), ("moonep_load8", 2), ("moonep_swiglu_save8", 0),
                                         ("moonep_swiglu_save8", 1), ("moonep_swiglu_backward8", 2),
                                         ("moonep_swiglu_backward8", 5), ("moonep_swiglu_backward8", 6),
-                                        ("moonep_dispatch8", 5), ("moonep_combine_backward_ungated", 2),
+                                        ("moonep_dispatch8", 5), ("moonep_combine_backward_ungated", 0),
+                                        ("moonep_combine_backward_ungated", 2), ("moonep_layernorm_backward", 0),
+                                        ("moonep_layernorm_backward8", 0), ("moonep_layernorm_backward8", 5),
                                         ("moonep_layernorm", 0), ("moonep_layernorm", 3),
                                         ("moonep_layernorm_backward", 1)])
 def test_rows_off_their_elements_alignment(name, which):
