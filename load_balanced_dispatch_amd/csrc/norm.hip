@@ -535,16 +535,18 @@ RowShape bwd_shape(int H) {
 }
 
 // Every block of the backward leaves a partial sum of 2 H floats, so it launches fewer than fit: 8 waves to a
-// CU reach the rate of 16 (2048 columns 127 us against 136, 7168 the same), and at least 4 rows to a wave or block.
+// CU reach the rate of 16 (2048 columns 127 us against 136, 7168 the same), and beyond a block to a CU at least 4 rows
+// to a wave or block (1024 rows of 1024 columns: 8.5 us, 10.5 with 4 rows always; 4096 of them: 13.2, 14.5 with 2).
 constexpr int kBwdWavesPerCU = 8;
 constexpr int kMinRows = 4;
 
 // Blocks of the backward, which are also the partial sums it leaves.
 unsigned bwd_blocks(int64_t rows, const RowShape& q) {
   const int64_t groups = q.lanes == 64 ? (rows + 3) / 4 : rows;
-  const int64_t need = (groups + kMinRows - 1) / kMinRows;
+  const int64_t cus = device_cu_count(), deep = (groups + kMinRows - 1) / kMinRows;
+  const int64_t need = groups < cus ? groups : deep < cus ? cus : deep;
   const int waves = q.lanes == 64 ? 4 : q.lanes / 64;
-  const int64_t cap = (int64_t)device_cu_count() * (waves < kBwdWavesPerCU ? kBwdWavesPerCU / waves : 1);
+  const int64_t cap = cus * (waves < kBwdWavesPerCU ? kBwdWavesPerCU / waves : 1);
   return (unsigned)(need < cap ? need : cap);
 }
 
