@@ -199,8 +199,6 @@ class MoeFFN:
             self.Xn = torch.empty((R, S, H), **act)
             self.mean = torch.empty((R, S), **f32)
             self.rstd = torch.empty((R, S), **f32)
-        else:
-            self.Xn = self.X
         rows = {"Xp": (N, H), "Ygu": (N, 2 * Hp), "A": (N, Hp), "Zp": (N, H)}
         if save8:  # the backward's rows of these shapes take the places of Zp and Ygu
             rows.update(dA=(N, Hp), dXp=(N, H))
@@ -242,8 +240,6 @@ class MoeFFN:
                 self.dbeta = torch.zeros(H, **f32)
                 self.ws_norm = torch.empty(max(1, _lib.moonep_layernorm_backward_workspace_bytes(d, H)),
                                            dtype=torch.uint8, device=device)
-            else:
-                self.dXn = self.dX
             self.dW_gu_home = torch.zeros((E, H, 2 * Hp), **f32)
             self.dW_gu_slots = torch.zeros((R, B, H, 2 * Hp), **f32)
             self.dW_down_home = torch.zeros((E, Hp, H), **f32)
@@ -271,7 +267,7 @@ class MoeFFN:
         elif self.save8:
             calls.append(("save8", lambda: L.moonep_save8(d.R * d.S, H, self.X, self.x_codes, self.x_exps)))
         calls += [
-            ("dispatch", lambda: L.moonep_dispatch(d, H, self.Xn, self.dest_idx, self.Xp)),
+            ("dispatch", lambda: L.moonep_dispatch(d, H, self.Xn if self.norm else self.X, self.dest_idx, self.Xp)),
             ("gemm_gate_up", lambda: L.moonep_group_gemm(d, H, 2 * Hp, self.Xp, self.W_gu_home, sl(self.W_gu_slots),
                                                          self.cu_seqlens, self.Ygu, self.ws_gemm)),
             ("swiglu_save8", lambda: L.moonep_swiglu_save8(d, Hp, self.Ygu, self.A, self.ygu_codes, self.ygu_exps))
@@ -318,7 +314,8 @@ class MoeFFN:
                                                                 self.ws_gemm)),
             ("wgrad_gate_up", lambda: L.moonep_wgrad(d, H, 2 * Hp, self.Xp, self.dYgu, self.cu_seqlens,
                                                      self.dW_gu_home, sl(self.dW_gu_slots), self.ws_wgrad)),
-            ("dispatch_backward", lambda: L.moonep_dispatch_backward(d, H, self.dXp, self.dest_idx, self.dXn)),
+            ("dispatch_backward", lambda: L.moonep_dispatch_backward(d, H, self.dXp, self.dest_idx,
+                                                                     self.dXn if self.norm else self.dX)),
             ("reduce_grad", lambda: (L.moonep_reduce_grad(d, H, 2 * Hp, sl(self.slot_expert), self.dW_gu_home,
                                                           sl(self.dW_gu_slots)),
                                      L.moonep_reduce_grad(d, Hp, H, sl(self.slot_expert), self.dW_down_home,

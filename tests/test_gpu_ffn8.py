@@ -172,6 +172,23 @@ def test_norm_without_checkpoints_against_the_plain_ffn(m):
     assert_gemm_close(np64(L.dbeta), db, 1e-4, "dbeta")
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(norm=True), dict(norm=True, save8=True)])
+def test_buffers_given_by_assignment(m, kw):
+    # a program may put its own tensors in the place of the layer's
+    a, b = (m.MoeFFN(*DIMS, backward=True, **kw) for _ in range(2))
+    for L in (a, b):
+        fill(L, 45)
+    b.X, b.dX, b.dout = b.X.clone(), torch.empty_like(b.dX), b.dout.clone()
+    a.X.zero_()
+    fill(a, 45)
+    for L in (a, b):
+        L.forward()
+        L.backward()
+    torch.cuda.synchronize()
+    ga, gb = grads(a), grads(b)
+    assert all(torch.equal(ga[n], gb[n]) for n in ga)
+
+
 def test_layers_share_their_row_buffers(m):
     alone = [m.MoeFFN(*DIMS, backward=True, norm=True, save8=True) for _ in range(2)]
     first = m.MoeFFN(*DIMS, backward=True, norm=True, save8=True)
