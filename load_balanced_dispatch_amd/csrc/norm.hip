@@ -240,22 +240,26 @@ struct ZFrom8 {
   }
 };
 
-// Persistent: a lane keeps its columns from row to row, and with them gamma and the sums of dy z and dy
-// over its rows, which the block leaves in part [gridDim.x, 2, H] (WAVE: summed over its four waves).
-// The next row's loads are issued before the current row's stores: loads and stores retire in one order,
-// and a load behind the stores would wait for them.
-template <typename Z, bool AL, int NC, int MAXT, bool AHEAD>
-__global__ __launch_bounds__(MAXT) void layernorm_bwd_rows(const float* __restrict__ dY, Z src,
-                                                                        const float* __restrict__ rstd,
-                                                                        const float* __restrict__ gamma,
-                                                                        float* __restrict__ dX,
-                                                                        float* __restrict__ part, int64_t rows,
-                                                                        int H) {
-  constexpr bool WAVE = MAXT == 256;
-  constexpr bool KEEP = NC < 8;  // gamma in registers
+// How a block's waves share its rows: a wave to a row and four rows at a time, all waves to a row, or groups of
+// `waves` waves to a row and several rows at a time.
+enum Share { kWaves4, kBlock, kGroups };
+
+// Persistent: a lane keeps its columns from row to row, and with them gamma and the sums of dy z and dy over its
+// rows, which the block adds up over its rows at a time and leaves in part [gridDim.x, 2, H].  The next row's loads
+// are issued before the current row's stores: loads and stores retire in one order, and a load behind the
+// stores would wait for them.
+template <typename Z, bool AL, int NC, Share SHARE, bool AHEAD>
+__global__ __launch_bounds__(SHARE == kWaves4 ? 256 : 1024) void layernorm_bwd_rows(
+    const float* __restrict__ dY, Z src, const float* __restrict__ rstd, const float* __restrict__ gamma,
+    float* __restrict__ dX, float* __restrict__ part, int64_t rows, int H, int waves_arg) {
+  constexpr bool KEEP = NC < 8;    // gamma in registers
+  extern __shared__ f32x4 fold[];  // [groups - 1][NC][lanes]
   __shared__ float lds[2][2][16];
-  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, lanes = WAVE ? 64 : blockDim.x;
-  const int64_t step = WAVE ? (int64_t)gridDim.x * 4 : gridDim.x;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = SHARE == kWaves4 ? 1 : SHARE == kBlock ? blockDim.x >> 6 : waves_arg;
+  const int groups = SHARE == kWaves4 ? 4 : SHARE == kBlock ? 1 : (int)(blockDim.x >> 6) / waves;
+  const int group = SHARE == kWaves4 ? wave : SHARE == kBlock ? 0 : wave / waves;
+  const int lanes = waves * 64, t = threadIdx.x - group * lanes;
   const float inv_h = 1.f / (float)H;
   f32x4 w[KEEP ? NC : 1], dg[NC], db[NC];
   auto weight = [&](int c) { return KEEP ? w[KEEP ? c : 0] : load4<AL>(gamma, (c * lanes + t) * kQuad, H); };
@@ -281,86 +285,89 @@ __global__ __launch_bounds__(MAXT) void layernorm_bwd_rows(const float* __restri
     }
   };
   int flip = 0;
-  int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
   Loaded cur, next;
   if (AHEAD && row < rows) load(row, cur);
-  for (; row < rows; row += step) {
-    if (!AHEAD) load(row, cur);
-    else if (row + step < rows) load(row + step, next);
+  // with groups the block goes on until none of them has a row, since they share its barriers
+  for (int64_t first = SHARE == kGroups ? row - group : row; first < rows; first += step, row += step) {
+    const bool live = SHARE != kGroups || row < rows;
+    if (!AHEAD) {
+      if (live) load(row, cur);
+    } else if (row + step < rows) {
+      load(row + step, next);
+    }
     f32x4 z[NC];
     float s1 = 0.f, s2 = 0.f;
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      z[c] = src.z(cur.q[c], cur.row, cur.r);
-      const f32x4 g = weight(c);
+      for (int c = 0; c < NC; ++c) {
+        z[c] = src.z(cur.q[c], cur.row, cur.r);
+        const f32x4 g = weight(c);
 #pragma unroll
-      for (int i = 0; i < kQuad; ++i) {
-        if (!AL && (c * lanes + t) * kQuad + i >= H) z[c][i] = 0.f;
-        const float gy = cur.dy[c][i] * g[i];
-        s1 += gy;
-        s2 = __builtin_fmaf(gy, z[c][i], s2);
-        dg[c][i] = __builtin_fmaf(cur.dy[c][i], z[c][i], dg[c][i]);
-        db[c][i] += cur.dy[c][i];
+        for (int i = 0; i < kQuad; ++i) {
+          if (!AL && (c * lanes + t) * kQuad + i >= H) z[c][i] = 0.f;
+          const float gy = cur.dy[c][i] * g[i];
+          s1 += gy;
+          s2 = __builtin_fmaf(gy, z[c][i], s2);
+          dg[c][i] = __builtin_fmaf(cur.dy[c][i], z[c][i], dg[c][i]);
+          db[c][i] += cur.dy[c][i];
+        }
       }
+      s1 = wave_sum(s1);
+      s2 = wave_sum(s2);
     }
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
-    if constexpr (!WAVE) {
+    if constexpr (SHARE != kWaves4) {
       // two sets of slots, so that one barrier a row is enough
       if ((threadIdx.x & 63) == 0) {
-        lds[flip][0][threadIdx.x >> 6] = s1;
-        lds[flip][1][threadIdx.x >> 6] = s2;
+        lds[flip][0][wave] = s1;
+        lds[flip][1][wave] = s2;
       }
       __syncthreads();
       s1 = s2 = 0.f;
-      const int nw = blockDim.x >> 6;
-      for (int k = 0; k < nw; ++k) {
+      for (int k = group * waves; k < group * waves + waves; ++k) {
         s1 += lds[flip][0][k];
         s2 += lds[flip][1][k];
       }
       flip ^= 1;
     }
-    s1 *= inv_h;
-    s2 *= inv_h;
+    if (live) {
+      s1 *= inv_h;
+      s2 *= inv_h;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const f32x4 g = weight(c);
-      f32x4 dx;
+      for (int c = 0; c < NC; ++c) {
+        const f32x4 g = weight(c);
+        f32x4 dx;
 #pragma unroll
-      for (int i = 0; i < kQuad; ++i)
-        dx[i] = cur.r * (__builtin_fmaf(cur.dy[c][i], g[i], -s1) - z[c][i] * s2);
-      store4<AL>(dX + row * H, (c * lanes + t) * kQuad, H, dx);
+        for (int i = 0; i < kQuad; ++i)
+          dx[i] = cur.r * (__builtin_fmaf(cur.dy[c][i], g[i], -s1) - z[c][i] * s2);
+        store4<AL>(dX + row * H, (c * lanes + t) * kQuad, H, dx);
+      }
     }
     if (AHEAD) cur = next;
   }
   float* out = part + (int64_t)blockIdx.x * 2 * H;
-  if constexpr (WAVE) {
-    __shared__ f32x4 fold[3][NC * 64];
-    for (int k = 0; k < 2; ++k) {
-      if (k) __syncthreads();
-      if (threadIdx.x >= 64) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) fold[(threadIdx.x >> 6) - 1][c * 64 + t] = k ? db[c] : dg[c];
+  for (int k = 0; k < 2; ++k) {
+    if constexpr (SHARE != kBlock) {
+      if (k) __syncthreads();
+      if (group > 0) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) fold[((group - 1) * NC + c) * lanes + t] = k ? db[c] : dg[c];
       }
       __syncthreads();
-      if (threadIdx.x < 64) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int at = c * 64 + t;
-          f32x4 v = k ? db[c] : dg[c];
-#pragma unroll
-          for (int j = 0; j < 3; ++j)
-#pragma unroll
-            for (int i = 0; i < kQuad; ++i) v[i] += fold[j][at][i];
-          store4<AL>(out + k * H, at * kQuad, H, v);
-        }
-      }
     }
-  } else {
+    if (group == 0) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      store4<AL>(out, (c * lanes + t) * kQuad, H, dg[c]);
-      store4<AL>(out + H, (c * lanes + t) * kQuad, H, db[c]);
+      for (int c = 0; c < NC; ++c) {
+        f32x4 v = k ? db[c] : dg[c];
+        for (int j = 0; j + 1 < groups; ++j) {
+          const f32x4 o = fold[(j * NC + c) * lanes + t];
+#pragma unroll
+          for (int i = 0; i < kQuad; ++i) v[i] += o[i];
+        }
+        store4<AL>(out + k * H, (c * lanes + t) * kQuad, H, v);
+      }
     }
   }
 }
@@ -521,33 +528,40 @@ RowShape fwd_shape(int H) {
 // fill in (measured: 62 us against 63, 127 against 130 on 2048 and 4096 columns).
 constexpr int kFwdWavesPerCU = 64;
 
-// Backward, chunks of 4 columns.  Measured on 32 768 rows of 7168 columns from the checkpoint: 392 us with 14
-// waves of 2 chunks against 408 with 7 of 4 (128 registers then hold no second row), 422 with 7 of 4
-// loading each row when it is needed; one wave of 4 chunks against 4 of 1 on 1024 columns: 69 us against 93.
-RowShape bwd_shape(int H) {
+// Backward, chunks of 4 columns: chunks per lane, waves to a row, rows at a time, and how many waves the launch gives a
+// CU.  Every block leaves a partial sum of 2 H floats, so there are fewer than fit, and several rows share
+// one.  Measured (rows from the checkpoint): to 1024 columns one wave of 4 chunks, 32 768 rows of 1024 in 65 us
+// against 93 with 4 waves of one; to 2560 columns groups of 3 to 5 waves, 3711 rows of 1408 in 16.4 us against
+// 18.8 and 32 768 of 2048 in 114 against 122 with blocks of one row; beyond, where at most two groups
+// fit, all waves to a row: 1024 rows of 4096 14.8 us against 16.6, 32 768 of 7168 380 us with 14 waves of 2
+// chunks against 395 with 7 of 4 (128 registers then hold no second row).
+struct BwdShape {
+  int nc, waves, groups;
+  Share share;
+  int waves_per_cu;
+};
+
+BwdShape bwd_shape(int H) {
   const int nch = (H + kQuad - 1) / kQuad;
-  if (nch <= 64) return {1, 64};
-  if (nch <= 128) return {2, 64};
-  if (nch <= 256) return {4, 64};
-  if (nch <= 2048) return {2, ((nch + 127) / 128) * 64};
-  if (nch <= 4096) return {4, ((nch + 255) / 256) * 64};
-  return {8, ((nch + 511) / 512) * 64};
+  if (nch <= 256) return {nch <= 64 ? 1 : nch <= 128 ? 2 : 4, 1, 4, kWaves4, 8};
+  const int waves = (nch + 127) / 128;
+  if (nch <= 640) return {2, waves, 16 / waves, kGroups, 16};
+  if (nch <= 2048) return {2, waves, 1, kBlock, 8};
+  if (nch <= 4096) return {4, (nch + 255) / 256, 1, kBlock, 16};
+  return {8, (nch + 511) / 512, 1, kBlock, 16};
 }
 
-// Every block of the backward leaves a partial sum of 2 H floats, so it launches fewer than fit: 8 waves to a
-// CU reach the rate of 16 (2048 columns 127 us against 136, 7168 the same), and beyond a block to a CU at least 4 rows
-// to a wave or block (1024 rows of 1024 columns: 8.5 us, 10.5 with 4 rows always; 4096 of them: 13.2, 14.5 with 2).
-constexpr int kBwdWavesPerCU = 8;
+// Beyond a block to a CU, at least 4 rows to a wave or group (1024 rows of 1024 columns: 8.5 us, 10.5 with 4 rows
+// always; 4096 of them: 13.2, 14.5 with 2).
 constexpr int kMinRows = 4;
 
 // Blocks of the backward, which are also the partial sums it leaves.
-unsigned bwd_blocks(int64_t rows, const RowShape& q) {
-  const int64_t groups = q.lanes == 64 ? (rows + 3) / 4 : rows;
-  const int64_t cus = device_cu_count(), deep = (groups + kMinRows - 1) / kMinRows;
-  const int64_t need = groups < cus ? groups : deep < cus ? cus : deep;
-  const int waves = q.lanes == 64 ? 4 : q.lanes / 64;
-  const int64_t cap = cus * (waves < kBwdWavesPerCU ? kBwdWavesPerCU / waves : 1);
-  return (unsigned)(need < cap ? need : cap);
+unsigned bwd_blocks(int64_t rows, const BwdShape& q) {
+  const int64_t need = (rows + q.groups - 1) / q.groups, deep = (need + kMinRows - 1) / kMinRows;
+  const int64_t cus = device_cu_count();
+  const int64_t cap = cus * (q.waves_per_cu / (q.waves * q.groups) > 0 ? q.waves_per_cu / (q.waves * q.groups) : 1);
+  const int64_t blocks = need < cus ? need : deep < cus ? cus : deep;
+  return (unsigned)(blocks < cap ? blocks : cap);
 }
 
 template <typename T, bool AL, bool PAST>
@@ -598,24 +612,20 @@ void layernorm_bwd_launch(int64_t rows, int H, const float* dY, Z z, const float
                          (int)rows, H, row_blocks);
     return;
   }
-  const RowShape q = bwd_shape(H);
+  const BwdShape q = bwd_shape(H);
   const unsigned grid = bwd_blocks(rows, q);
-  const dim3 block(q.lanes == 64 ? 256 : q.lanes);
-#define MOONEP_LNB(NC, MAXT, AHEAD)                                                                                \
-  hipLaunchKernelGGL((layernorm_bwd_rows<Z, AL, NC, MAXT, AHEAD>), dim3(grid), block, 0, s, dY, z, rstd, gamma, dX, part, \
-                     rows, H)
-  if (q.lanes == 64) {
-    if (q.nc == 1) MOONEP_LNB(1, 256, true);
-    else if (q.nc == 2) MOONEP_LNB(2, 256, true);
-    else MOONEP_LNB(4, 256, true);
-
-  } else if (q.nc == 2) {
-    MOONEP_LNB(2, 1024, true);
-  } else if (q.nc == 4) {
-    MOONEP_LNB(4, 1024, false);
-  } else {
-    MOONEP_LNB(8, 1024, false);
-  }
+  const dim3 block(q.waves * q.groups * 64);
+  const size_t fold = (size_t)(q.groups - 1) * q.nc * q.waves * 64 * sizeof(f32x4);
+#define MOONEP_LNB(NC, SHARE, AHEAD)                                                                              \
+  hipLaunchKernelGGL((layernorm_bwd_rows<Z, AL, NC, SHARE, AHEAD>), dim3(grid), block, fold, s, dY, z, rstd, gamma, \
+                     dX, part, rows, H, q.waves)
+  if (q.share == kGroups) MOONEP_LNB(2, kGroups, true);
+  else if (q.share == kWaves4 && q.nc == 1) MOONEP_LNB(1, kWaves4, true);
+  else if (q.share == kWaves4 && q.nc == 2) MOONEP_LNB(2, kWaves4, true);
+  else if (q.share == kWaves4) MOONEP_LNB(4, kWaves4, true);
+  else if (q.nc == 2) MOONEP_LNB(2, kBlock, true);
+  else if (q.nc == 4) MOONEP_LNB(4, kBlock, false);
+  else MOONEP_LNB(8, kBlock, false);
 #undef MOONEP_LNB
   hipLaunchKernelGGL(layernorm_fold, dim3(ceil_div_u(H, 64), dbeta ? 2 : 1), dim3(kFoldWaves * 64), 0, s, part,
                      (int)grid, H, dgamma, dbeta);

@@ -375,14 +375,14 @@ def test_layernorm_backward(m, dtype, H):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32, "8"])
-@pytest.mark.parametrize("H", [1, 7, 64, 253, 512, 1000, 1024, 1413, 2048, 2500, 7168, 8192, 16384, 20001, 32768])
+@pytest.mark.parametrize("H", [1, 7, 64, 253, 512, 1000, 1024, 1413, 2048, 2500, 2560, 4096, 7168, 8192, 16384, 20001, 32768])
 def test_layernorm_backward_more_rows(m, dtype, H):
     # more than 512 rows: the rows' blocks leave partial sums, a second launch folds them
     backward_case(m, dtype, H, 3, 173)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 63, 64, 65, 256, 257, 511, 512, 513])
-@pytest.mark.parametrize("H", [72, 520])
+@pytest.mark.parametrize("rows", [1, 2, 63, 64, 65, 256, 257, 511, 512, 513, 1027, 2051])
+@pytest.mark.parametrize("H", [72, 520, 1100, 1413, 2050, 2560, 2564])
 def test_layernorm_backward_row_counts(m, rows, H):
     backward_case(m, BF, H, 1, rows)
 
