@@ -304,3 +304,67 @@ def test_activation_is_the_plain_ones_bit_for_bit(m, dtype):
     torch.cuda.synchronize()
     same = (a == b) | (torch.isnan(a) & torch.isnan(b))
     assert bool(same.all())
+
+
+def test_offsets_past_32_bits(m):
+    # 310 000 rows of 7168 columns are 2.2e9 elements: the last rows must be those of a call on them alone
+    n, H, last = 310_000, 7168, 6
+    g = torch.Generator(device=DEV).manual_seed(9)
+    gamma, beta = rand_tensor((H,), F32, 2), rand_tensor((H,), F32, 3)
+
+    def norm(x):
+        rows = x.shape[0]
+        d = m.make_dims(1, 1, 0, rows, 1)
+        Y, v, Xp = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        rstd = torch.empty(rows, device=DEV)
+        codes = torch.empty((rows, H), dtype=torch.int8, device=DEV)
+        exps = torch.empty((rows, H // 32), dtype=torch.uint8, device=DEV)
+        m.moonep_layernorm(d, H, x, gamma, beta, 1e-5, Y, None, rstd, codes, exps)
+        m.moonep_load8(rows, H, codes, exps, v)
+        m.moonep_dispatch8(d, H, codes, exps, gamma, beta, torch.arange(rows, dtype=torch.int32, device=DEV), Xp)
+        return Y, v, Xp, codes, exps, rstd
+
+    x = torch.randn((n, H), generator=g, device=DEV, dtype=BF)
+    say("norm, load8, dispatch8 of", n, "rows")
+    whole = norm(x)
+    tail = norm(x[-last:].clone())
+    for a, b in zip(whole, tail):
+        assert torch.equal(a[-last:], b)
+    codes, exps, rstd = whole[3:]
+    del whole, x
+    dY = torch.randn((n, H), generator=g, device=DEV)
+
+    def back(rows, dY_, codes_, exps_, rstd_):
+        d = m.make_dims(1, 1, 0, rows, 1)
+        dX, dg, Xp = torch.empty_like(dY_), torch.zeros(H, device=DEV), torch.empty((rows, H), dtype=BF, device=DEV)
+        ws = torch.empty(m.moonep_layernorm_backward_workspace_bytes(d, H), dtype=torch.uint8, device=DEV)
+        m.moonep_layernorm_backward8(d, H, dY_, codes_, exps_, rstd_, gamma, dX, dg, None, ws)
+        m.moonep_combine_backward_ungated(d, H, dY_, torch.arange(rows, dtype=torch.int32, device=DEV), Xp)
+        return dX, Xp
+
+    say("norm backward, ungated rows of", n, "rows")
+    dX, Xp = back(n, dY, codes, exps, rstd)
+    dXt, Xpt = back(last, dY[-last:].clone(), codes[-last:].clone(), exps[-last:].clone(), rstd[-last:].clone())
+    assert torch.equal(Xp[-last:], Xpt)
+    # few rows take another kernel, which sums the means in another order: 65 u of the terms (test_gpu_norm8.py)
+    z = np64(tail[1])
+    gy = np.abs(np64(dY[-last:]) * np64(gamma))
+    terms = gy + gy.mean(axis=1, keepdims=True) + np.abs(z) * (gy * np.abs(z)).mean(axis=1, keepdims=True)
+    tol = 2 * 65 * 2.0 ** -24 * np64(rstd[-last:])[:, None] * terms
+    assert np.all(np.abs(np64(dX[-last:]) - np64(dXt)) <= tol)
+    del dX, Xp, dY, codes, exps
+    Hp = H // 2
+    y = torch.randn((n, 2 * Hp), generator=g, device=DEV, dtype=BF)
+
+    def act(rows, y_):
+        d = m.make_dims(1, 1, 0, rows, 1)
+        A, A2, dYgu = (torch.empty((rows, w), dtype=BF, device=DEV) for w in (Hp, Hp, 2 * Hp))
+        c = torch.empty((rows, 2, Hp), dtype=torch.int8, device=DEV)
+        e = torch.empty((rows, 2, Hp // 32), dtype=torch.uint8, device=DEV)
+        m.moonep_swiglu_save8(d, Hp, y_, A, c, e)
+        m.moonep_swiglu_backward8(d, Hp, c, e, A, None, None, A2, dYgu, None)
+        return A, c, e, A2, dYgu
+
+    say("swiglu_save8, swiglu_backward8 of", n, "rows")
+    for a, b in zip(act(n, y), act(last, y[-last:].clone())):
+        assert torch.equal(a[-last:], b)
