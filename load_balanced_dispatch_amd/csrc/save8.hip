@@ -27,6 +27,7 @@ namespace {
 // 512), its backward, 262 144 x 2048, 901 us (909, 938).  Rows off their alignment run fastest in large ones, whose
 // waves share the lines at the ends of their pieces in one L1: 32 768 x 1413, 160 us (168 with 256, 181 with 128).
 constexpr int stream_threads(bool al) { return al ? 64 : 512; }
+constexpr int load8_threads(bool al) { return al ? 128 : 512; }  // 4096 x 2048: 6.5 us, 7.6 with 64; large ones the same
 constexpr int bwd8_threads(bool al) { return al ? 64 : 256; }
 constexpr int kScatterThreads = 128;  // 262 144 x 7168 rows of an output gradient: 852 us, 857 with 64, 884 with 256
 
@@ -58,10 +59,10 @@ __global__ __launch_bounds__(stream_threads(AL)) void save8_rows(const T* __rest
 }
 
 template <typename T, bool AL, bool PAST>
-__global__ __launch_bounds__(stream_threads(AL)) void load8_rows(const int8_t* __restrict__ codes,
+__global__ __launch_bounds__(load8_threads(AL)) void load8_rows(const int8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ exps, T* __restrict__ X,
                                                        int64_t rows, int C) {
-  constexpr int kT = stream_threads(AL);
+  constexpr int kT = load8_threads(AL);
   const int nb = (C + kBlock8 - 1) / kBlock8, nc = chunks8(C);
   const int64_t total = rows * nc;
   for (int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x; i < total; i += (int64_t)gridDim.x * kT) {
@@ -272,7 +273,7 @@ int rows_launch(const char* name, bool save, int64_t rows, int C, const void* X,
     if (al) hipLaunchKernelGGL((save8_rows<T, true>), grid, block, 0, s, x, c, e, rows, C);
     else hipLaunchKernelGGL((save8_rows<T, false>), grid, block, 0, s, x, c, e, rows, C);
   } else {
-    const dim3 grid(grid_for(rows * chunks8(C), stream_threads(al))), block(stream_threads(al));
+    const dim3 grid(grid_for(rows * chunks8(C), load8_threads(al))), block(load8_threads(al));
     T* x = static_cast<T*>(Xout);
 #define MOONEP_LOAD8(AL, PAST) \
   hipLaunchKernelGGL((load8_rows<T, AL, PAST>), grid, block, 0, s, c, e, x, rows, C)
