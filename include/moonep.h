@@ -345,8 +345,9 @@ int moonep_load8(int64_t rows, int32_t C, moonep_dtype t, const int8_t* codes, c
                  moonep_stream stream);
 
 /*
- * moonep_swiglu_save8 -- moonep_swiglu (the same A, bit for bit), and its input kept in 8 bits in the same pass.  Each
- *   row's gate and up halves are coded as rows of their own: the codes are those of moonep_save8 of Ygu as [2*R*S*K, Hp].
+ * moonep_swiglu_save8 -- moonep_swiglu (the same A, bit for bit), and its input kept in 8 bits in the same pass.
+ *   Each row's gate and up halves are coded as rows of their own: the codes are those of moonep_save8 of Ygu as
+ *   [2*R*S*K, Hp].
  * In:  Ygu [R*S*K, 2*Hp] dtype t.
  * Out: A [R*S*K, Hp] dtype t;  codes [R*S*K, 2, Hp] int8;  exps [R*S*K, 2, moonep_save8_blocks(Hp)] uint8.
  */

@@ -575,8 +575,8 @@ void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, con
   const T* x = static_cast<const T*>(X);
   T* y = static_cast<T*>(Y);
 #define MOONEP_LN(NC, MAXT, KEEP)                                                                               \
-  hipLaunchKernelGGL((layernorm_rows<T, AL, PAST, NC, MAXT, KEEP>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, mean, \
-                     rstd, codes, exps, rows, H)
+  hipLaunchKernelGGL((layernorm_rows<T, AL, PAST, NC, MAXT, KEEP>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, \
+                     mean, rstd, codes, exps, rows, H)
   if (q.lanes == 64) {
     if (q.nc == 1) MOONEP_LN(1, 256, true);
     else MOONEP_LN(2, 256, true);
@@ -695,7 +695,8 @@ extern "C" int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype 
   MOONEP_REQUIRE(aligned_to(dY, 4) && aligned_to(dX, 4), "%s: a row pointer is not aligned to its elements", name);
   MOONEP_REQUIRE(aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", name);
   hipStream_t s = as_stream(stream);
-  const bool al = H % kQuad == 0 && aligned_to(X, t == MOONEP_BF16 ? 8 : 16) && aligned16(dY) && aligned16(dX) && aligned16(gamma);
+  const bool al = H % kQuad == 0 && aligned_to(X, t == MOONEP_BF16 ? 8 : 16) && aligned16(dY) && aligned16(dX) &&
+                  aligned16(gamma);
   const int64_t rows = (int64_t)d.R * d.S;
   float* part = static_cast<float*>(workspace);
   clear_stale_error();

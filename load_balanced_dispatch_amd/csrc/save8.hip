@@ -27,7 +27,7 @@ namespace {
 // 512), its backward, 262 144 x 2048, 901 us (909, 938).  Rows off their alignment run fastest in large ones, whose
 // waves share the lines at the ends of their pieces in one L1: 32 768 x 1413, 160 us (168 with 256, 181 with 128).
 constexpr int stream_threads(bool al) { return al ? 64 : 512; }
-constexpr int load8_threads(bool al) { return al ? 128 : 512; }  // 4096 x 2048: 6.5 us, 7.6 with 64; large ones the same
+constexpr int load8_threads(bool al) { return al ? 128 : 512; }  // 4096 x 2048: 6.5 us, 7.6 with 64; larger the same
 constexpr int bwd8_threads(bool al) { return al ? 64 : 256; }
 constexpr int kScatterThreads = 128;  // 262 144 x 7168 rows of an output gradient: 852 us, 857 with 64, 884 with 256
 
@@ -76,8 +76,8 @@ __global__ __launch_bounds__(load8_threads(AL)) void load8_rows(const int8_t* __
 
 // ------------------------------------------------------------------ activation
 
-// 1 / x for x in [1, 2]: the hardware's reciprocal and a Newton step, which gives the correctly rounded quotient (checked
-// on the device for every float32 there) without the general division's handling of other ranges; the
+// 1 / x for x in [1, 2]: the hardware's reciprocal and a Newton step, which gives the correctly rounded quotient
+// (checked on the device for every float32 there) without the general division's handling of other ranges; the
 // activation with its checkpoint took 365 us so, 388 with the division (196 608 x 1408).
 __device__ __forceinline__ float recip_1_2(float x) {
   const float r = __builtin_amdgcn_rcpf(x);
@@ -255,8 +255,8 @@ void scatter_launch(bool al, const int32_t* dest, void* Xp, const moonep_dims& d
   const int pieces = (chunks8(C) + 63) / 64;
   const unsigned grid = grid_for(tokens * pieces * 64, kScatterThreads);
 #define MOONEP_SCATTER(AL, PAST)                                                                        \
-  hipLaunchKernelGGL((scatter_rows<T, AL, PAST, Src<AL>>), dim3(grid), dim3(kScatterThreads), 0, s, Src<AL>{args...}, dest, \
-                     static_cast<T*>(Xp), tokens, d.K, C, pieces)
+  hipLaunchKernelGGL((scatter_rows<T, AL, PAST, Src<AL>>), dim3(grid), dim3(kScatterThreads), 0, s, \
+                     Src<AL>{args...}, dest, static_cast<T*>(Xp), tokens, d.K, C, pieces)
   MOONEP_BY_ROWS(T, al, n_pairs(d) * C * (int64_t)sizeof(T), MOONEP_SCATTER);
 #undef MOONEP_SCATTER
 }

@@ -222,8 +222,8 @@ __device__ __forceinline__ void decode(u32x2 q, float step, float (&f)[kChunk]) 
 
 // ------------------------------------------------------------------ host side
 
-// Whether rows of type T, `bytes` of them, are written past the caches (PAST).  The call that follows reads it, from the
-// 256 MB last-level cache where it still is there: norm and dispatch of 32 768 x 2048 (134 MB) took 237 us
+// Whether rows of type T, `bytes` of them, are written past the caches (PAST).  The call that follows reads them, from
+// the 256 MB last-level cache where they still are there: norm and dispatch of 32 768 x 2048 (134 MB) took 237 us
 // with ordinary stores of the norm's rows and 243 with non-temporal ones, of 32 768 x 7168 (470 MB) 1043 and
 // 1028; alone, the kernels here run 4-15% faster with non-temporal stores.
 template <typename T>
