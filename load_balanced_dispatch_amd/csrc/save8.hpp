@@ -14,8 +14,8 @@
 // value.  b = 255 (an infinity or NaN in the block) makes every value of the block NaN, so that a
 // step that overflowed is seen by the backward pass as it would be with the values kept whole.
 //
-// Kernels give a lane 8 columns (16 bytes of bf16) and a block a quad of lanes, so the block's largest
-// magnitude takes two DPP moves.  Each kernel is built twice: AL for rows whose 8-column chunks are
+// Kernels give a lane 8 columns (16 bytes of bf16; the norm's backward, whose rows are float32, 4) and a
+// block a quad of lanes, so the block's largest magnitude takes two DPP moves.  Each kernel is built twice: AL for rows whose 8-column chunks are
 // whole and aligned, and without for any width and alignment, with the same wide accesses at element
 // alignment and a last chunk element by element.
 #pragma once
