@@ -209,8 +209,9 @@ def test_layers_share_their_row_buffers(m):
         assert all(torch.equal(ga[n], gb[n]) for n in ga)
 
 
-def test_captured_and_replayed(m):
-    L, E = (m.MoeFFN(*DIMS, backward=True, norm=True, save8=True) for _ in range(2))
+@pytest.mark.parametrize("dims", [DIMS, (4, 16, 2, 160, 4, 256, 192)])  # the norm's backward in one launch, in two
+def test_captured_and_replayed(m, dims):
+    L, E = (m.MoeFFN(*dims, backward=True, norm=True, save8=True) for _ in range(2))
     sums = lambda x: [x.dW_gu_home, x.dW_down_home, x.dgamma, x.dbeta]  # noqa: E731
 
     def step(x):
