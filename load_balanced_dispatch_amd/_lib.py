@@ -337,55 +337,53 @@ def moonep_swiglu_backward(d: Dims, Hp: int, Ygu, dA, dYgu, stream=None):
 # ------------------------------------------------------------------ layer norm and 8-bit checkpoints
 import torch  # noqa: E402  (already loaded with the library)
 
+_Tensor = torch.Tensor
 
-class _Call:
-    """Checks the tensors of one call, which must all lie on one device, and makes it on that device's current
-    stream (or the one passed), whatever device is current."""
 
-    __slots__ = ("device",)
+def _launch(entry, *args, stream=None):
+    """Calls `entry` with its arguments, tensors given as (tensor, name, dtype, elements) and passed as pointers, on the
+    current stream of the device that they all lie on (or the stream passed), whatever device is current."""
+    device, values = None, []
+    for a in args:
+        if a.__class__ is tuple:
+            t, name, dtype, numel = a
+            # what every tensor after the first passes by, if nothing is wrong with it
+            if not (t.__class__ is _Tensor and t.dtype is dtype and t.numel() == numel and t.is_contiguous()
+                    and t.get_device() == device):
+                _ptr(t, name, dtype, numel)
+                at = t.get_device()
+                if device is None:
+                    device = at
+                elif at != device:
+                    raise ValueError(f"{name} is on cuda:{at}, the tensors before it on cuda:{device}")
+            a = t.data_ptr()
+        values.append(a)
+    if stream is None:
+        # the handle alone: torch.cuda.current_stream() costs 2-3 us, as much as a small kernel
+        values.append(torch._C._cuda_getCurrentRawStream(device))
+    elif stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    else:
+        values.append(stream.cuda_stream)
+    if device == torch._C._cuda_getDevice():
+        rc = entry(*values)
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*values)
+    if rc != MOONEP_OK:
+        _check(rc)
 
-    def __init__(self):
-        self.device = -1  # index, once a tensor has set it
 
-    @staticmethod
-    def dtype(t, name):
-        """The row type of a tensor that sets the call's, and the library's code for it."""
-        if t is None:
-            raise ValueError(f"{name} is required")
-        return t.dtype, _dtype_enum(t)
+def _row_type(t, name):
+    """The row type of the tensor that sets the call's, and the library's code for it."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t.dtype, _dtype_enum(t)
 
-    def ptr(self, t, name, dtype, numel, optional=False):
-        if t is None and optional:
-            return None
-        if not (t.__class__ is torch.Tensor and t.is_cuda and t.is_contiguous() and t.dtype is dtype
-                and t.numel() == numel):
-            _ptr(t, name, dtype, numel)  # says what is wrong (or that nothing is: a subclass, no dtype to hold to)
-        device = t.get_device()
-        if device != self.device:
-            if self.device >= 0:
-                raise ValueError(f"{name} is on cuda:{device}, the tensors before it on cuda:{self.device}")
-            self.device = device
-        return t.data_ptr()
 
-    def workspace(self, t, needed):
-        p = self.ptr(t, "workspace", None, None)
-        if t.numel() * t.element_size() < needed:
-            raise ValueError(f"workspace too small: {needed} bytes needed")
-        return p
-
-    def __call__(self, entry, *args, stream=None):
-        if stream is None:
-            # the handle alone: torch.cuda.current_stream() costs 2-3 us, as much as a small kernel
-            handle = torch._C._cuda_getCurrentRawStream(self.device)
-        elif stream.device.index != self.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{self.device}")
-        else:
-            handle = stream.cuda_stream
-        if self.device == torch.cuda.current_device():
-            _check(entry(*args, handle))
-        else:
-            with torch.cuda.device(self.device):
-                _check(entry(*args, handle))
+def _or_none(t, *spec):
+    """An optional tensor's argument: None where it is not given."""
+    return None if t is None else (t, *spec)
 
 
 def moonep_save8_blocks(C: int) -> int:
@@ -393,108 +391,96 @@ def moonep_save8_blocks(C: int) -> int:
     return int(_LIB.moonep_save8_blocks(int(C)))
 
 
-def _codes(c, codes, exps, rows, C, optional=False):
-    """Pointers of 8-bit rows [rows, C]."""
-    return (c.ptr(codes, "codes", torch.int8, rows * C, optional),
-            c.ptr(exps, "exps", torch.uint8, rows * moonep_save8_blocks(C), optional))
+def _rows8(codes, exps, rows, C):
+    """8-bit rows [rows, C] as arguments."""
+    return (codes, "codes", torch.int8, rows * C), (exps, "exps", torch.uint8, rows * -(-C // 32))
 
 
 def moonep_save8(rows: int, C: int, X, codes, exps, stream=None):
     """Keeps X [rows, C] in 8 bits: codes int8 [rows, C], exps uint8 [rows, moonep_save8_blocks(C)]."""
-    c = _Call()
-    t, code = c.dtype(X, "X")
-    x = c.ptr(X, "X", t, rows * C)
-    c(_LIB.moonep_save8, int(rows), int(C), code, x, *_codes(c, codes, exps, rows, C), stream=stream)
+    t, code = _row_type(X, "X")
+    _launch(_LIB.moonep_save8, int(rows), int(C), code, (X, "X", t, rows * C), *_rows8(codes, exps, rows, C),
+            stream=stream)
 
 
 def moonep_load8(rows: int, C: int, codes, exps, X, stream=None):
     """Writes the values of 8-bit rows to X [rows, C] (bfloat16 or float32, both exact)."""
-    c = _Call()
-    t, code = c.dtype(X, "X")
-    x = c.ptr(X, "X", t, rows * C)
-    c(_LIB.moonep_load8, int(rows), int(C), code, *_codes(c, codes, exps, rows, C), x, stream=stream)
+    t, code = _row_type(X, "X")
+    _launch(_LIB.moonep_load8, int(rows), int(C), code, *_rows8(codes, exps, rows, C), (X, "X", t, rows * C),
+            stream=stream)
 
 
 def moonep_swiglu_save8(d: Dims, Hp: int, Ygu, A, codes, exps, stream=None):
     """moonep_swiglu, and Ygu kept in 8 bits (its gate and up halves as rows of their own)."""
-    c = _Call()
     N = d.N
-    t, code = c.dtype(Ygu, "Ygu")
-    y = c.ptr(Ygu, "Ygu", t, N * 2 * Hp)
-    a = c.ptr(A, "A", t, N * Hp)
-    c(_LIB.moonep_swiglu_save8, d, int(Hp), code, y, a, *_codes(c, codes, exps, 2 * N, Hp), stream=stream)
+    t, code = _row_type(Ygu, "Ygu")
+    _launch(_LIB.moonep_swiglu_save8, d, int(Hp), code, (Ygu, "Ygu", t, N * 2 * Hp), (A, "A", t, N * Hp),
+            *_rows8(codes, exps, 2 * N, Hp), stream=stream)
 
 
 def moonep_swiglu_backward8(d: Dims, Hp: int, codes, exps, dA, src_of_row, gates, A, dYgu, dgates, stream=None):
     """Gradient of moonep_swiglu from its 8-bit input; with src_of_row, gates and dgates (all or none) the gates
     are applied here: A and dYgu come out times the gate, and dgates is <dA, silu(g) u> per pair."""
-    c = _Call()
     N = d.N
-    t, code = c.dtype(dA, "dA")
-    rows8 = _codes(c, codes, exps, 2 * N, Hp)
-    c(_LIB.moonep_swiglu_backward8, d, int(Hp), code, *rows8, c.ptr(dA, "dA", t, N * Hp),
-      c.ptr(src_of_row, "src_of_row", torch.int32, N, optional=True),
-      c.ptr(gates, "gates", torch.float32, N, optional=True), c.ptr(A, "A", t, N * Hp),
-      c.ptr(dYgu, "dYgu", t, N * 2 * Hp), c.ptr(dgates, "dgates", torch.float32, N, optional=True), stream=stream)
+    t, code = _row_type(dA, "dA")
+    _launch(_LIB.moonep_swiglu_backward8, d, int(Hp), code, *_rows8(codes, exps, 2 * N, Hp), (dA, "dA", t, N * Hp),
+            _or_none(src_of_row, "src_of_row", torch.int32, N), _or_none(gates, "gates", torch.float32, N),
+            (A, "A", t, N * Hp), (dYgu, "dYgu", t, N * 2 * Hp), _or_none(dgates, "dgates", torch.float32, N),
+            stream=stream)
 
 
 def moonep_dispatch8(d: Dims, H: int, codes, exps, gamma, beta, dest_idx, Xp, stream=None):
     """moonep_dispatch from 8-bit token rows, times gamma plus beta (float32 [H], or None)."""
-    c = _Call()
-    t, code = c.dtype(Xp, "Xp")
-    rows8 = _codes(c, codes, exps, d.R * d.S, H)
-    c(_LIB.moonep_dispatch8, d, int(H), code, *rows8, c.ptr(gamma, "gamma", torch.float32, H, True),
-      c.ptr(beta, "beta", torch.float32, H, True), c.ptr(dest_idx, "dest_idx", torch.int32, d.N),
-      c.ptr(Xp, "Xp", t, d.N * H), stream=stream)
+    t, code = _row_type(Xp, "Xp")
+    _launch(_LIB.moonep_dispatch8, d, int(H), code, *_rows8(codes, exps, d.R * d.S, H),
+            _or_none(gamma, "gamma", torch.float32, H), _or_none(beta, "beta", torch.float32, H),
+            (dest_idx, "dest_idx", torch.int32, d.N), (Xp, "Xp", t, d.N * H), stream=stream)
 
 
 def moonep_combine_backward_ungated(d: Dims, D: int, dout, dest_idx, dYp, stream=None):
     """The output gradient's rows laid out by expert, without gates."""
-    c = _Call()
-    t, code = c.dtype(dYp, "dYp")
-    c(_LIB.moonep_combine_backward_ungated, d, int(D), code,
-      c.ptr(dout, "dout", torch.float32, d.R * d.S * D), c.ptr(dest_idx, "dest_idx", torch.int32, d.N),
-      c.ptr(dYp, "dYp", t, d.N * D), stream=stream)
+    t, code = _row_type(dYp, "dYp")
+    _launch(_LIB.moonep_combine_backward_ungated, d, int(D), code, (dout, "dout", torch.float32, d.R * d.S * D),
+            (dest_idx, "dest_idx", torch.int32, d.N), (dYp, "dYp", t, d.N * D), stream=stream)
 
 
 def moonep_layernorm(d: Dims, H: int, X, gamma, beta, eps: float, Y, mean, rstd, codes=None, exps=None, stream=None):
     """Layer norm of X [R,S,H]; mean and rstd [R,S] may be None, and codes and exps keep the normalised rows in
     8 bits."""
-    c = _Call()
-    t, code = c.dtype(X, "X")
+    t, code = _row_type(X, "X")
     T, f32 = d.R * d.S, torch.float32
-    c(_LIB.moonep_layernorm, d, int(H), code, c.ptr(X, "X", t, T * H), c.ptr(gamma, "gamma", f32, H),
-      c.ptr(beta, "beta", f32, H, optional=True), float(eps), c.ptr(Y, "Y", t, T * H),
-      c.ptr(mean, "mean", f32, T, optional=True), c.ptr(rstd, "rstd", f32, T, optional=True),
-      *_codes(c, codes, exps, T, H, optional=True), stream=stream)
+    c8, e8 = _rows8(codes, exps, T, H)
+    _launch(_LIB.moonep_layernorm, d, int(H), code, (X, "X", t, T * H), (gamma, "gamma", f32, H),
+            _or_none(beta, "beta", f32, H), float(eps), (Y, "Y", t, T * H), _or_none(mean, "mean", f32, T),
+            _or_none(rstd, "rstd", f32, T), None if codes is None else c8, None if exps is None else e8, stream=stream)
 
 
 def moonep_layernorm_backward_workspace_bytes(d: Dims, H: int) -> int:
     return int(_LIB.moonep_layernorm_backward_workspace_bytes(d, int(H)))
 
 
-def _layernorm_backward(c, entry, d, H, dtype, dY, z, rstd, gamma, dX, dgamma, dbeta, workspace, stream):
+def _layernorm_backward(entry, d, H, code, dY, z, rstd, gamma, dX, dgamma, dbeta, workspace, stream):
     T, f32 = d.R * d.S, torch.float32
-    c(entry, d, int(H), *dtype, c.ptr(dY, "dY", f32, T * H), *z, c.ptr(rstd, "rstd", f32, T),
-      c.ptr(gamma, "gamma", f32, H), c.ptr(dX, "dX", f32, T * H), c.ptr(dgamma, "dgamma", f32, H),
-      c.ptr(dbeta, "dbeta", f32, H, optional=True),
-      c.workspace(workspace, moonep_layernorm_backward_workspace_bytes(d, H)), stream=stream)
+    if workspace is not None:
+        needed = moonep_layernorm_backward_workspace_bytes(d, H)
+        if workspace.numel() * workspace.element_size() < needed:
+            raise ValueError(f"workspace too small: {needed} bytes needed")
+    _launch(entry, d, int(H), *code, (dY, "dY", f32, T * H), *z, (rstd, "rstd", f32, T), (gamma, "gamma", f32, H),
+            (dX, "dX", f32, T * H), (dgamma, "dgamma", f32, H), _or_none(dbeta, "dbeta", f32, H),
+            (workspace, "workspace", None, None), stream=stream)
 
 
 def moonep_layernorm_backward(d: Dims, H: int, dY, X, mean, rstd, gamma, dX, dgamma, dbeta, workspace, stream=None):
     """Gradients of moonep_layernorm from its input: writes dX, adds into dgamma and dbeta (or None)."""
-    c = _Call()
-    t, code = c.dtype(X, "X")
+    t, code = _row_type(X, "X")
     T = d.R * d.S
-    z = (c.ptr(X, "X", t, T * H), c.ptr(mean, "mean", torch.float32, T))
-    _layernorm_backward(c, _LIB.moonep_layernorm_backward, d, H, (code,), dY, z, rstd, gamma, dX, dgamma,
-                        dbeta, workspace, stream)
+    _layernorm_backward(_LIB.moonep_layernorm_backward, d, H, (code,), dY,
+                        ((X, "X", t, T * H), (mean, "mean", torch.float32, T)), rstd, gamma, dX, dgamma, dbeta,
+                        workspace, stream)
 
 
 def moonep_layernorm_backward8(d: Dims, H: int, dY, codes, exps, rstd, gamma, dX, dgamma, dbeta, workspace,
                                stream=None):
     """moonep_layernorm_backward from the 8-bit normalised rows."""
-    c = _Call()
-    z = _codes(c, codes, exps, d.R * d.S, H)
-    _layernorm_backward(c, _LIB.moonep_layernorm_backward8, d, H, (), dY, z, rstd, gamma, dX, dgamma, dbeta,
-                        workspace, stream)
+    _layernorm_backward(_LIB.moonep_layernorm_backward8, d, H, (), dY, _rows8(codes, exps, d.R * d.S, H), rstd, gamma,
+                        dX, dgamma, dbeta, workspace, stream)
