@@ -407,6 +407,16 @@ int moonep_layernorm(moonep_dims d, int32_t H, moonep_dtype t, const void* X, co
                      float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* exps,
                      moonep_stream stream);
 
+/*
+ * moonep_layernorm_dispatch -- moonep_layernorm and moonep_dispatch of its rows in one pass: Xp[dest_idx[r,s,k], :] =
+ *   Y[r,s,:] of moonep_layernorm (the same bits), Y itself is not stored; rows with dest -1 are skipped.
+ * In:  as moonep_layernorm;  dest_idx [R,S,K] int32 from moonep_plan.
+ * Out: Xp [R*S*K, H] dtype t;  mean, rstd, codes, exps as moonep_layernorm.
+ */
+int moonep_layernorm_dispatch(moonep_dims d, int32_t H, moonep_dtype t, const void* X, const float* gamma,
+                              const float* beta, float eps, const int32_t* dest_idx, void* Xp, float* mean,
+                              float* rstd, int8_t* codes, uint8_t* exps, moonep_stream stream);
+
 /* Bytes of device workspace moonep_layernorm_backward and moonep_layernorm_backward8 need on the current device. */
 size_t moonep_layernorm_backward_workspace_bytes(moonep_dims d, int32_t H);
 

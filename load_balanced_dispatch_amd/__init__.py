@@ -6,8 +6,9 @@ moonep_dispatch, moonep_prefetch, moonep_group_gemm, moonep_combine,
 moonep_wgrad, moonep_reduce_grad -- three for the backward of the data path --
 moonep_combine_backward, moonep_group_gemm_dgrad, moonep_dispatch_backward --
 two for the activation of the gated expert FFN -- moonep_swiglu,
-moonep_swiglu_backward -- three for the layer norm in front of it --
-moonep_layernorm, moonep_layernorm_backward, moonep_layernorm_backward8 -- and
+moonep_swiglu_backward -- four for the layer norm in front of it --
+moonep_layernorm, moonep_layernorm_dispatch, moonep_layernorm_backward,
+moonep_layernorm_backward8 -- and
 the 8-bit activation checkpoints -- moonep_save8, moonep_load8,
 moonep_swiglu_save8, moonep_swiglu_backward8, moonep_dispatch8,
 moonep_combine_backward_ungated -- exposed here under the same names, taking
@@ -24,7 +25,8 @@ from ._lib import (  # noqa: F401
     moonep_combine_backward, moonep_group_gemm_dgrad, moonep_dispatch_backward, moonep_swiglu,
     moonep_swiglu_backward,
     moonep_save8_blocks, moonep_save8, moonep_load8, moonep_swiglu_save8, moonep_swiglu_backward8, moonep_dispatch8,
-    moonep_combine_backward_ungated, moonep_layernorm, moonep_layernorm_backward_workspace_bytes,
+    moonep_combine_backward_ungated, moonep_layernorm, moonep_layernorm_dispatch,
+    moonep_layernorm_backward_workspace_bytes,
     moonep_layernorm_backward, moonep_layernorm_backward8,
 )
 from .layer import MoeFFN  # noqa: F401

@@ -83,6 +83,7 @@ def _load():
         "moonep_dispatch8": (ctypes.c_int, [Dims, i32, ctypes.c_int] + [vp] * 7),
         "moonep_combine_backward_ungated": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, vp]),
         "moonep_layernorm": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, ctypes.c_float] + [vp] * 6),
+        "moonep_layernorm_dispatch": (ctypes.c_int, [Dims, i32, ctypes.c_int, vp, vp, vp, ctypes.c_float] + [vp] * 7),
         "moonep_layernorm_backward_workspace_bytes": (sz, [Dims, i32]),
         "moonep_layernorm_backward": (ctypes.c_int, [Dims, i32, ctypes.c_int] + [vp] * 10),
         "moonep_layernorm_backward8": (ctypes.c_int, [Dims, i32] + [vp] * 10),
@@ -103,7 +104,7 @@ SYMBOLS = ("moonep_last_error", "moonep_plan_workspace_bytes", "moonep_plan", "m
            "moonep_wgrad_workspace_bytes", "moonep_wgrad", "moonep_reduce_grad", "moonep_combine_backward",
            "moonep_group_gemm_dgrad", "moonep_dispatch_backward", "moonep_swiglu", "moonep_swiglu_backward",
            "moonep_save8_blocks", "moonep_save8", "moonep_load8", "moonep_swiglu_save8", "moonep_swiglu_backward8",
-           "moonep_dispatch8", "moonep_combine_backward_ungated", "moonep_layernorm",
+           "moonep_dispatch8", "moonep_combine_backward_ungated", "moonep_layernorm", "moonep_layernorm_dispatch",
            "moonep_layernorm_backward_workspace_bytes", "moonep_layernorm_backward", "moonep_layernorm_backward8")
 
 
@@ -453,6 +454,18 @@ def moonep_layernorm(d: Dims, H: int, X, gamma, beta, eps: float, Y, mean, rstd,
     _launch(_LIB.moonep_layernorm, d, int(H), code, (X, "X", t, T * H), (gamma, "gamma", f32, H),
             _or_none(beta, "beta", f32, H), float(eps), (Y, "Y", t, T * H), _or_none(mean, "mean", f32, T),
             _or_none(rstd, "rstd", f32, T), None if codes is None else c8, None if exps is None else e8, stream=stream)
+
+
+def moonep_layernorm_dispatch(d: Dims, H: int, X, gamma, beta, eps: float, dest_idx, Xp, mean, rstd, codes=None,
+                              exps=None, stream=None):
+    """moonep_layernorm and moonep_dispatch of its rows in one pass; the normalised rows themselves are not stored."""
+    t, code = _row_type(X, "X")
+    T, f32 = d.R * d.S, torch.float32
+    c8, e8 = _rows8(codes, exps, T, H)
+    _launch(_LIB.moonep_layernorm_dispatch, d, int(H), code, (X, "X", t, T * H), (gamma, "gamma", f32, H),
+            _or_none(beta, "beta", f32, H), float(eps), (dest_idx, "dest_idx", torch.int32, d.N),
+            (Xp, "Xp", t, d.N * H), _or_none(mean, "mean", f32, T), _or_none(rstd, "rstd", f32, T),
+            None if codes is None else c8, None if exps is None else e8, stream=stream)
 
 
 def moonep_layernorm_backward_workspace_bytes(d: Dims, H: int) -> int:

@@ -5,7 +5,8 @@
 //   dx = r (gy - mean(gy) - z mean(gy z)),  gy = dy gamma
 //   dgamma += sum over rows of dy z,  dbeta += sum over rows of dy
 // The forward can write z in 8 bits (save8.hpp) in the same pass; the backward then reads that instead
-// of x, and moonep_dispatch8 makes the expert inputs from it again.
+// of x, and moonep_dispatch8 makes the expert inputs from it again.  moonep_layernorm_dispatch writes y straight
+// to its pairs' places (32 768 rows of 2048 columns to 6 places each: 200 us, 239 as two calls).
 //
 // A row is read from HBM once and held in registers by one wave or by all waves of a block; sums run over
 // lanes with DPP moves, over waves through LDS, always in the same order.
@@ -47,13 +48,15 @@ __device__ __forceinline__ float row_sum(float x, float* lds) {
 }
 
 // MAXT = 256: a wave per row, four rows to a block.  Otherwise a block per row.  KEEP: persistent, with gamma and
-// beta in registers from row to row and the next row's loads issued before the current row's stores.
-template <typename T, bool AL, bool PAST, int NC, int MAXT, bool KEEP>
+// beta in registers from row to row and the next row's loads issued before the current row's stores.  SCATTER: the
+// rows go to their pairs' places dest [rows, K] in Y, as dispatch lays them out, and not to their own.
+template <typename T, bool AL, bool PAST, int NC, int MAXT, bool KEEP, bool SCATTER>
 __global__ __launch_bounds__(MAXT) void layernorm_rows(const T* __restrict__ X, const float* __restrict__ gamma,
                                                        const float* __restrict__ beta, float eps, T* __restrict__ Y,
                                                        float* __restrict__ mean, float* __restrict__ rstd,
                                                        int8_t* __restrict__ codes, uint8_t* __restrict__ exps,
-                                                       int64_t rows, int H) {
+                                                       const int32_t* __restrict__ dest, int K, int64_t rows,
+                                                       int H) {
   constexpr bool WAVE = MAXT == 256;
   __shared__ float lds[2][16];
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, lanes = WAVE ? 64 : blockDim.x;
@@ -123,7 +126,14 @@ __global__ __launch_bounds__(MAXT) void layernorm_rows(const T* __restrict__ X, 
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) y[i] = __builtin_fmaf(x[c][i], w[i], y[i]);
       }
-      store_chunk<AL, PAST>(Y + row * H, col, H, y);
+      if constexpr (SCATTER) {
+        for (int k = 0; k < K; ++k) {
+          const int32_t to = dest[row * K + k];
+          if (to >= 0) store_chunk<AL, PAST>(Y + (int64_t)to * H, col, H, y);
+        }
+      } else {
+        store_chunk<AL, PAST>(Y + row * H, col, H, y);
+      }
     }
     if (t == 0) {
       if (mean != nullptr) mean[row] = m;
@@ -564,9 +574,10 @@ unsigned bwd_blocks(int64_t rows, const BwdShape& q) {
   return (unsigned)(blocks < cap ? blocks : cap);
 }
 
-template <typename T, bool AL, bool PAST>
+template <typename T, bool AL, bool PAST, bool SCATTER>
 void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, const float* gamma, const float* beta,
-                      float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* exps, hipStream_t s) {
+                      float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* exps, const int32_t* dest,
+                      int K, hipStream_t s) {
   const int64_t need = q.lanes == 64 ? (rows + 3) / 4 : rows;
   const int waves = q.lanes == 64 ? 4 : q.lanes / 64;
   const int64_t cap = (int64_t)device_cu_count() * (kFwdWavesPerCU / waves);
@@ -575,8 +586,8 @@ void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, con
   const T* x = static_cast<const T*>(X);
   T* y = static_cast<T*>(Y);
 #define MOONEP_LN(NC, MAXT, KEEP)                                                                               \
-  hipLaunchKernelGGL((layernorm_rows<T, AL, PAST, NC, MAXT, KEEP>), dim3(grid), block, 0, s, x, gamma, beta, eps, y, \
-                     mean, rstd, codes, exps, rows, H)
+  hipLaunchKernelGGL((layernorm_rows<T, AL, PAST, NC, MAXT, KEEP, SCATTER>), dim3(grid), block, 0, s, x, gamma, \
+                     beta, eps, y, mean, rstd, codes, exps, dest, K, rows, H)
   if (q.lanes == 64) {
     if (q.nc == 1) MOONEP_LN(1, 256, true);
     else MOONEP_LN(2, 256, true);
@@ -636,9 +647,42 @@ int check_width(const char* name, int32_t H) {
   return MOONEP_OK;
 }
 
-int bwd_checks(const char* name, const moonep_dims& d, int32_t H) {
+int norm_checks(const char* name, const moonep_dims& d, int32_t H) {
   if (int rc = check_dims(d, name)) return rc;
   return check_width(name, H);
+}
+
+// moonep_layernorm, and with SCATTER moonep_layernorm_dispatch, whose Y is Xp.
+template <bool SCATTER>
+int layernorm_entry(const char* name, const moonep_dims& d, int32_t H, moonep_dtype t, const void* X,
+                    const float* gamma, const float* beta, float eps, const int32_t* dest, void* Y, float* mean,
+                    float* rstd, int8_t* codes, uint8_t* exps, moonep_stream stream) {
+  if (int rc = norm_checks(name, d, H)) return rc;
+  MOONEP_REQUIRE(t == MOONEP_F32 || t == MOONEP_BF16, "%s: bad dtype %d", name, (int)t);
+  MOONEP_REQUIRE(eps > 0.f && eps <= 3.4e38f, "%s: eps must be positive and finite", name);
+  MOONEP_REQUIRE(aligned_to(X, elem_bytes(t)) && aligned_to(Y, elem_bytes(t)),
+                 "%s: a row pointer is not aligned to its elements", name);
+  MOONEP_REQUIRE((codes == nullptr) == (exps == nullptr), "%s: codes and exps go together", name);
+  const int64_t rows = (int64_t)d.R * d.S;
+  if (rows == 0) return MOONEP_OK;
+  MOONEP_REQUIRE(X && gamma && Y && (dest || !SCATTER), "%s: null pointer", name);
+  hipStream_t s = as_stream(stream);
+  clear_stale_error();
+  const RowShape q = fwd_shape(H);
+  const bool al = H % kChunk == 0 && aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
+                  aligned_to(codes, 8);
+#define MOONEP_LN(T, AL, PAST)                                                                                      \
+  layernorm_launch<T, AL, PAST, SCATTER>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, dest, d.K, s)
+#define MOONEP_LN_BF16(AL, PAST) MOONEP_LN(uint16_t, AL, PAST)
+#define MOONEP_LN_F32(AL, PAST) MOONEP_LN(float, AL, PAST)
+  const int64_t bytes = (SCATTER ? n_pairs(d) : rows) * H * (int64_t)elem_bytes(t);
+  if (t == MOONEP_BF16) MOONEP_BY_ROWS(uint16_t, al, bytes, MOONEP_LN_BF16);
+  else MOONEP_BY_ROWS(float, al, bytes, MOONEP_LN_F32);
+#undef MOONEP_LN
+#undef MOONEP_LN_BF16
+#undef MOONEP_LN_F32
+  MOONEP_LAUNCH_CHECK(name);
+  return MOONEP_OK;
 }
 
 }  // namespace
@@ -649,37 +693,19 @@ using namespace moonep;
 extern "C" int moonep_layernorm(moonep_dims d, int32_t H, moonep_dtype t, const void* X, const float* gamma,
                                 const float* beta, float eps, void* Y, float* mean, float* rstd, int8_t* codes,
                                 uint8_t* exps, moonep_stream stream) {
-  const char* name = "moonep_layernorm";
-  if (int rc = bwd_checks(name, d, H)) return rc;
-  MOONEP_REQUIRE(t == MOONEP_F32 || t == MOONEP_BF16, "%s: bad dtype %d", name, (int)t);
-  MOONEP_REQUIRE(eps > 0.f && eps <= 3.4e38f, "%s: eps must be positive and finite", name);
-  MOONEP_REQUIRE(aligned_to(X, elem_bytes(t)) && aligned_to(Y, elem_bytes(t)),
-                 "%s: a row pointer is not aligned to its elements", name);
-  MOONEP_REQUIRE((codes == nullptr) == (exps == nullptr), "%s: codes and exps go together", name);
-  const int64_t rows = (int64_t)d.R * d.S;
-  if (rows == 0) return MOONEP_OK;
-  MOONEP_REQUIRE(X && gamma && Y, "%s: null pointer", name);
-  hipStream_t s = as_stream(stream);
-  clear_stale_error();
-  const RowShape q = fwd_shape(H);
-  const bool al = H % kChunk == 0 && aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
-                  aligned_to(codes, 8);
-#define MOONEP_LN(T, AL, PAST) \
-  layernorm_launch<T, AL, PAST>(q, rows, H, X, gamma, beta, eps, Y, mean, rstd, codes, exps, s)
-#define MOONEP_LN_BF16(AL, PAST) MOONEP_LN(uint16_t, AL, PAST)
-#define MOONEP_LN_F32(AL, PAST) MOONEP_LN(float, AL, PAST)
-  const int64_t bytes = rows * H * (int64_t)elem_bytes(t);
-  if (t == MOONEP_BF16) MOONEP_BY_ROWS(uint16_t, al, bytes, MOONEP_LN_BF16);
-  else MOONEP_BY_ROWS(float, al, bytes, MOONEP_LN_F32);
-#undef MOONEP_LN
-#undef MOONEP_LN_BF16
-#undef MOONEP_LN_F32
-  MOONEP_LAUNCH_CHECK(name);
-  return MOONEP_OK;
+  return layernorm_entry<false>("moonep_layernorm", d, H, t, X, gamma, beta, eps, nullptr, Y, mean, rstd, codes, exps,
+                                stream);
+}
+
+extern "C" int moonep_layernorm_dispatch(moonep_dims d, int32_t H, moonep_dtype t, const void* X, const float* gamma,
+                                         const float* beta, float eps, const int32_t* dest_idx, void* Xp, float* mean,
+                                         float* rstd, int8_t* codes, uint8_t* exps, moonep_stream stream) {
+  return layernorm_entry<true>("moonep_layernorm_dispatch", d, H, t, X, gamma, beta, eps, dest_idx, Xp, mean, rstd,
+                               codes, exps, stream);
 }
 
 extern "C" size_t moonep_layernorm_backward_workspace_bytes(moonep_dims d, int32_t H) {
-  if (bwd_checks("moonep_layernorm_backward_workspace_bytes", d, H) != MOONEP_OK) return 0;
+  if (norm_checks("moonep_layernorm_backward_workspace_bytes", d, H) != MOONEP_OK) return 0;
   return (size_t)bwd_blocks((int64_t)d.R * d.S, bwd_shape(H)) * 2 * H * sizeof(float);
 }
 
@@ -687,7 +713,7 @@ extern "C" int moonep_layernorm_backward(moonep_dims d, int32_t H, moonep_dtype 
                                          const float* mean, const float* rstd, const float* gamma, float* dX,
                                          float* dgamma, float* dbeta, void* workspace, moonep_stream stream) {
   const char* name = "moonep_layernorm_backward";
-  if (int rc = bwd_checks(name, d, H)) return rc;
+  if (int rc = norm_checks(name, d, H)) return rc;
   MOONEP_REQUIRE(t == MOONEP_F32 || t == MOONEP_BF16, "%s: bad dtype %d", name, (int)t);
   MOONEP_REQUIRE(aligned_to(X, elem_bytes(t)), "%s: a row pointer is not aligned to its elements", name);
   if ((int64_t)d.R * d.S == 0) return MOONEP_OK;
@@ -719,7 +745,7 @@ extern "C" int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float*
                                           const uint8_t* exps, const float* rstd, const float* gamma, float* dX,
                                           float* dgamma, float* dbeta, void* workspace, moonep_stream stream) {
   const char* name = "moonep_layernorm_backward8";
-  if (int rc = bwd_checks(name, d, H)) return rc;
+  if (int rc = norm_checks(name, d, H)) return rc;
   if ((int64_t)d.R * d.S == 0) return MOONEP_OK;
   MOONEP_REQUIRE(dY && codes && exps && rstd && gamma && dX && dgamma && workspace, "%s: null pointer", name);
   MOONEP_REQUIRE(aligned_to(dY, 4) && aligned_to(dX, 4), "%s: a row pointer is not aligned to its elements", name);

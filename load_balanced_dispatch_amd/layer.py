@@ -153,8 +153,9 @@ class MoeFFN:
     projections.  Every buffer has a shape fixed by (R, E, B, S, K, H, H'); nothing depends on the
     routing, so passes allocate nothing.
 
-    `norm=True` puts a layer norm (gamma, beta [H] float32, eps) in front: X is then its input, Xn what the
-    experts see, and backward() continues through it to dX, adding into dgamma and dbeta.
+    `norm=True` puts a layer norm (gamma, beta [H] float32, eps) in front: X is then its input, dispatch lays
+    out its rows in the same pass, and backward() continues through it from their gradient dXn to dX, adding into
+    dgamma and dbeta.
 
     `save8=True` (with backward=True) keeps only 8 bits of two activations from forward() to backward(): the
     rows that the experts read (normalised rows with norm=True, else X) in x_codes, x_exps [R, S, ...] and the
@@ -196,7 +197,6 @@ class MoeFFN:
         if norm:
             self.gamma = torch.ones(H, **f32)
             self.beta = torch.zeros(H, **f32)
-            self.Xn = torch.empty((R, S, H), **act)
             self.mean = torch.empty((R, S), **f32)
             self.rstd = torch.empty((R, S), **f32)
         rows = {"Xp": (N, H), "Ygu": (N, 2 * Hp), "A": (N, Hp), "Zp": (N, H)}
@@ -261,13 +261,15 @@ class MoeFFN:
                                                     sl(self.W_down_slots)))),
         ]
         if self.norm:
-            calls.append(("layernorm", lambda: L.moonep_layernorm(
-                d, H, self.X, self.gamma, self.beta, self.eps, self.Xn, self.mean, self.rstd,
-                self.x_codes if self.save8 else None, self.x_exps if self.save8 else None)))
-        elif self.save8:
-            calls.append(("save8", lambda: L.moonep_save8(d.R * d.S, H, self.X, self.x_codes, self.x_exps)))
+            dispatch = ("layernorm_dispatch", lambda: L.moonep_layernorm_dispatch(
+                d, H, self.X, self.gamma, self.beta, self.eps, self.dest_idx, self.Xp, self.mean, self.rstd,
+                self.x_codes if self.save8 else None, self.x_exps if self.save8 else None))
+        else:
+            dispatch = ("dispatch", lambda: L.moonep_dispatch(d, H, self.X, self.dest_idx, self.Xp))
+            if self.save8:
+                calls.append(("save8", lambda: L.moonep_save8(d.R * d.S, H, self.X, self.x_codes, self.x_exps)))
         calls += [
-            ("dispatch", lambda: L.moonep_dispatch(d, H, self.Xn if self.norm else self.X, self.dest_idx, self.Xp)),
+            dispatch,
             ("gemm_gate_up", lambda: L.moonep_group_gemm(d, H, 2 * Hp, self.Xp, self.W_gu_home, sl(self.W_gu_slots),
                                                          self.cu_seqlens, self.Ygu, self.ws_gemm)),
             ("swiglu_save8", lambda: L.moonep_swiglu_save8(d, Hp, self.Ygu, self.A, self.ygu_codes, self.ygu_exps))

@@ -351,6 +351,50 @@ def test_layernorm(m, dtype, H):
             assert np.all(np.abs(v - rz) <= np.where(near, 1.0, 0.5) * st + zb)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,K", [(1, 1), (40, 3), (253, 2), (512, 9), (1000, 4), (1413, 3), (2048, 6), (7168, 2),
+                                 (16392, 2)])
+def test_layernorm_dispatch_is_the_two_calls(m, dtype, H, K):
+    # bit for bit: the rows, the statistics and the checkpoint; rows without a destination are left alone
+    R, S, E = 2, 9, 16
+    p = oplanner.plan(random_routing(np.random.default_rng(H), R, S, K, E, 1.0), E, 1)
+    d = m.make_dims(R, E, 1, S, K)
+    dest = p.dest_idx.copy()
+    gone = int(dest[1, 3, 0])
+    dest[1, 3, 0] = -1
+    dest = i32(dest)
+    x = norm_rows(R * S, H, dtype, H)
+    gamma, beta = rand_tensor((H,), F32, 1), rand_tensor((H,), F32, 2)
+    nb = m.moonep_save8_blocks(H)
+    for by in (0, 1):
+        xo = at_offset(x, by)
+        outs = []
+        for fused in (False, True):
+            Xp = Guarded((d.N, H), dtype)
+            Xp.view.fill_(3.0)
+            mean, rstd = Guarded((R * S,), F32), Guarded((R * S,), F32)
+            codes, exps = Bytes((R * S, H), torch.int8, by), Bytes((R * S, nb), torch.uint8, by)
+            tail = (mean.view, rstd.view, codes.view, exps.view)
+            say("layernorm_dispatch" if fused else "layernorm, dispatch", dtype, H, K, "offset", by)
+            if fused:
+                m.moonep_layernorm_dispatch(d, H, xo, gamma, beta, 1e-5, dest, Xp.view, *tail)
+            else:
+                Y = torch.empty((R * S, H), dtype=dtype, device=DEV)
+                m.moonep_layernorm(d, H, xo, gamma, beta, 1e-5, Y, *tail)
+                m.moonep_dispatch(d, H, Y, dest, Xp.view)
+            torch.cuda.synchronize()
+            assert all(b.intact() for b in (Xp, mean, rstd, codes, exps))
+            outs.append((Xp.view, *tail))
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        assert bool((outs[1][0][gone] == 3.0).all())
+    Xp = torch.empty((d.N, H), dtype=dtype, device=DEV)
+    m.moonep_layernorm_dispatch(d, H, x, gamma, None, 1e-5, i32(p.dest_idx), Xp, None, None)
+    Y = torch.empty((R * S, H), dtype=dtype, device=DEV)
+    m.moonep_layernorm(d, H, x, gamma, None, 1e-5, Y, None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(Xp[torch.as_tensor(p.dest_idx.reshape(-1), device=DEV)], Y.repeat_interleave(K, 0))
+
+
 @pytest.mark.parametrize("H", [40, 253, 2048, 7168])
 def test_layernorm_checkpoint_is_save8_of_its_rows(m, H):
     # with weight 1 and no bias the float32 output is z itself, and the codes must be its 8-bit rows

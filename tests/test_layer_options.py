@@ -18,7 +18,7 @@ def test_calls_of_each_form():
              "reduce_grad"]
     assert names(make(backward=True)) == plain
     with_norm = names(make(backward=True, norm=True))
-    assert with_norm == plain[:2] + ["layernorm"] + plain[2:] + ["layernorm_backward"]
+    assert with_norm == plain[:2] + ["layernorm_dispatch"] + plain[3:] + ["layernorm_backward"]
     kept = names(make(backward=True, save8=True))
     assert kept[2] == "save8" and "swiglu_save8" in kept and "swiglu_backward8" in kept and "dispatch8" in kept
     assert "save8" not in names(make(backward=True, save8=True, norm=True))

@@ -21,6 +21,8 @@ CALLS = {
     "moonep_combine_backward_ungated":
         (lambda d, w, t, p: L.moonep_combine_backward_ungated(d, w, t, *p, None), 3, ()),
     "moonep_layernorm": (lambda d, w, t, p: L.moonep_layernorm(d, w, t, *p[:3], 1e-5, *p[3:], None), 8, (2, 4, 5)),
+    "moonep_layernorm_dispatch":
+        (lambda d, w, t, p: L.moonep_layernorm_dispatch(d, w, t, *p[:3], 1e-5, *p[3:], None), 9, (2, 5, 6)),
     "moonep_layernorm_backward": (lambda d, w, t, p: L.moonep_layernorm_backward(d, w, t, *p, None), 9, (7,)),
     "moonep_layernorm_backward8":
         (lambda d, w, t, p: L.moonep_layernorm_backward8(d, w, *p, None), 9, (7,)),
@@ -83,6 +85,7 @@ def test_arguments_that_go_together():
                                         ("moonep_combine_backward_ungated", 2), ("moonep_layernorm_backward", 0),
                                         ("moonep_layernorm_backward8", 0), ("moonep_layernorm_backward8", 5),
                                         ("moonep_layernorm", 0), ("moonep_layernorm", 3),
+                                        ("moonep_layernorm_dispatch", 0), ("moonep_layernorm_dispatch", 4),
                                         ("moonep_layernorm_backward", 1)])
 def test_rows_off_their_elements_alignment(name, which):
     call, n, _ = CALLS[name]
