@@ -525,11 +525,14 @@ struct RowShape {
 // Forward, chunks of 8 columns.  Two chunks a lane leave room to keep gamma and beta in registers and the next
 // row in flight.  Measured on 32 768 bf16 rows with a checkpoint: 2048 columns 63 us with 2 waves a row
 // against 84 with one wave of 4 chunks and 69 with 4 of 1; 7168 columns 221 us against 273 without
-// keeping anything between rows, and 342 with 14 waves of 1.
+// keeping anything between rows, and 342 with 14 waves of 1.  From 1025 to 1536 columns, where 2 waves of 2 would leave
+// a quarter and more of their lanes idle, 3 of 1 (1408 columns: 46.7 us against 48.3, 4096 rows of them 10.4 against
+// 11.1).
 RowShape fwd_shape(int H) {
   const int nch = chunks8(H);
   if (nch <= 64) return {1, 64};
   if (nch <= 128) return {2, 64};
+  if (nch <= 192) return {1, 192};
   if (nch <= 2048) return {2, ((nch + 127) / 128) * 64};
   return {4, ((nch + 255) / 256) * 64};
 }
@@ -591,6 +594,8 @@ void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, con
   if (q.lanes == 64) {
     if (q.nc == 1) MOONEP_LN(1, 256, true);
     else MOONEP_LN(2, 256, true);
+  } else if (q.nc == 1) {
+    MOONEP_LN(1, 1024, true);
   } else if (q.nc == 2) {
     MOONEP_LN(2, 1024, true);
   } else {
