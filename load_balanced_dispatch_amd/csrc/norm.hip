@@ -177,8 +177,9 @@ __device__ __forceinline__ void store4(float* p, int col, int H, f32x4 q) {
   }
 }
 
-// Where the backward reads z from: what it loads for a row and for a chunk, and z from them.  z past the
-// row's end is unspecified (dY is 0 there, and the sums leave it out).
+// Where the backward reads z from: what it loads for a row and for a chunk, and z from them.  Past the row's end x
+// reads as 0, so z is -mean * rstd there.  That can overflow although every z of the row is finite, and 0 * dY would
+// then be NaN: who sums over lanes past the end gives them an empty Row (mean 0, so z = 0) or sets z to 0.
 template <bool AL>
 struct ZFromBf16 {
   const uint16_t* X;
@@ -312,7 +313,8 @@ __global__ __launch_bounds__(SHARE == kWaves4 ? 256 : 1024) void layernorm_bwd_r
     if (live) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        z[c] = src.z(cur.q[c], cur.row, cur.r);
+        // aligned rows end with a chunk: lanes past the end have nothing of the row
+        z[c] = src.z(cur.q[c], AL && (c * lanes + t) * kQuad >= H ? typename Z::Row{} : cur.row, cur.r);
         const f32x4 g = weight(c);
 #pragma unroll
         for (int i = 0; i < kQuad; ++i) {
