@@ -102,13 +102,14 @@ size_t moonep_plan_workspace_bytes(moonep_dims d);
  * Out: expert_counts [E]        int32  T_e.
  *      maxvio        [1]        double.
  *      cu_seqlens    [R,E+B+1]  int32  rank r's group g occupies local rows
- *                                      [cu[r,g], cu[r,g+1]); cu[r,0]=0, cu[r,E+B]=P.
+ *                                      [cu[r,g], cu[r,g+1]); cu[r,0]=0, cu[r,E+B]=P
+ *                                      (less where ids outside [0,E) leave rows without a pair).
  *      slot_expert   [R,B]      int32  expert held by slot j of rank r, -1 unused
  *                                      (may be NULL when B == 0).
  *      dest_idx      [R,S,K]    int32  global row r'*P + local row of each pair;
  *                                      -1 for an id outside [0,E).
- *      src_of_row    [R*S*K]    int32  inverse of dest_idx (flat pair id per row),
- *                                      or NULL to skip.
+ *      src_of_row    [R*S*K]    int32  inverse of dest_idx (flat pair id per row, -1
+ *                                      for a row without a pair), or NULL to skip.
  *      stats         [4]        int32  copies (expert, non-home rank) used,
  *                                      of them slotted, of them direct reads,
  *                                      invalid ids + repeated ids within a token.

@@ -405,11 +405,19 @@ __global__ __launch_bounds__(kEmitThreads) void plan_emit(
     defe[r] = g_defend[r];
     efirst[r] = g_efirst[r];
   }
-  __syncthreads();
   const int per = E / R, G1 = E + B + 1;
   const int64_t tok0 = (int64_t)u * tpb;
   const int np = (int)min<int64_t>(tpb, tokens - tok0) * K;
   const int64_t base = tok0 * K;
+  if (src_of_row != nullptr) {
+    // rows past a rank's last group have no pair (ids outside [0, E) leave some); there are as many rows as
+    // pairs, so each block looks at the rows numbered like its pairs
+    for (int i = t; i < np; i += kEmitThreads) {
+      const int q = (int)base + i, d = q / P;
+      if (q - d * P >= cu[(int64_t)d * G1 + G1 - 1]) src_of_row[q] = -1;
+    }
+  }
+  __syncthreads();
   const int nbits = 32 - __clz(E);  // enough bits for the sentinel value E
   const uint64_t lt = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
   for (int tile = 0; tile < np; tile += kEmitThreads) {
