@@ -365,7 +365,8 @@ int moonep_swiglu_save8(moonep_dims d, int32_t Hp, moonep_dtype t, const void* Y
  *   moonep_combine_backward_ungated and multiplied by W_down^T (moonep_group_gemm_dgrad).  Then
  *   sum_c dA * h = <dout, Z> is the gate's gradient without Z, and moonep_wgrad of (A, the ungated rows) is
  *   the down projection's.  src_of_row, gates and dgates may all be NULL: w is then 1.  A row whose
- *   src_of_row is outside [0, R*S*K) counts as w = 0 and has no dgates; pairs without a row keep theirs.
+ *   src_of_row is outside [0, R*S*K) counts as w = 0 and has no dgates; pairs without a row (ids outside
+ *   [0, E)) keep theirs, so a caller that may have such pairs clears dgates first.
  * In:  codes [R*S*K, 2, Hp] int8, exps;  dA [R*S*K, Hp] dtype t;  src_of_row [R*S*K] int32 from moonep_plan;
  *      gates [R,S,K] float32.
  * Out: A [R*S*K, Hp], dYgu [R*S*K, 2*Hp] dtype t;  dgates [R,S,K] float32.

@@ -295,9 +295,11 @@ class MoeFFN:
                 ("combine_backward", lambda: L.moonep_combine_backward_ungated(d, H, self.dout, self.dest_idx,
                                                                                self.dZp)),
                 dgrad_down,
-                ("swiglu_backward8", lambda: L.moonep_swiglu_backward8(d, Hp, self.ygu_codes, self.ygu_exps, self.dA,
-                                                                       self.src_of_row, self.gates, self.A,
-                                                                       self.dYgu, self.dgates)),
+                # a pair whose id is outside [0, E) has no row, from which the call would write its gradient: it is 0
+                ("swiglu_backward8", lambda: (self.dgates.zero_(),
+                                              L.moonep_swiglu_backward8(d, Hp, self.ygu_codes, self.ygu_exps, self.dA,
+                                                                        self.src_of_row, self.gates, self.A,
+                                                                        self.dYgu, self.dgates))),
                 wgrad_down,
                 ("dispatch8", lambda: L.moonep_dispatch8(d, H, self.x_codes, self.x_exps, *affine, self.dest_idx,
                                                          self.Xp)),

@@ -75,3 +75,22 @@ def test_ffn_with_checkpoints_and_invalid_ids(m, dtype, norm):
             off = float((a[n].double() - b[n].double()).norm())
             assert off <= 0.05 * float(a[n].double().norm()), (step, n, off)
             assert torch.equal(b[n], c[n]), (step, n)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(save8=True), dict(save8=True, norm=True)])
+def test_gates_of_invalid_ids_have_no_gradient(m, kw):
+    # whatever an earlier step left there
+    L = m.MoeFFN(4, 16, 2, 128, 4, 256, 192, backward=True, **kw)
+    rng = np.random.default_rng(12)
+    for step in range(2):
+        ffn8.fill(L, 60 + step)
+        idx, bad = some_invalid(rng, npi(L.topk_idx), L.d.E, 0.2)
+        L.topk_idx.copy_(torch.as_tensor(idx.astype(np.int32)))
+        L.dgates.fill_(7.0)
+        say("FFN", kw, "gates of invalid ids, step", step)
+        L.forward()
+        L.backward()
+        torch.cuda.synchronize()
+        dropped = torch.as_tensor(bad, device=L.dgates.device)
+        assert not bool(L.dgates[dropped].any())
+        assert bool((L.dgates[~dropped] != 7.0).all())
