@@ -161,7 +161,8 @@ class MoeFFN:
     rows that the experts read (normalised rows with norm=True, else X) in x_codes, x_exps [R, S, ...] and the
     activation's input Ygu in ygu_codes, ygu_exps.  The row buffers of the forward pass are then free once it
     is over: they are in the dict `scratch`, which layers of one shape can share by passing one's to the
-    others' constructor (layers sharing it run one after another, as on one stream).  backward() applies the
+    others' constructor (layers sharing it run one after another, as on one stream).  A layer without a backward
+    has such a dict too; with backward=True and save8=False `scratch` is None.  backward() applies the
     gates on the experts' side: ungated output-gradient rows -> dgrad of the down projection -> swiglu backward
     from 8 bits (which also gives the gated activation and dgates) -> wgrad of the down projection -> dispatch
     from 8 bits -> dgrad and wgrad of the gate|up projection -> dispatch backward -> reduce_grad.
@@ -208,7 +209,8 @@ class MoeFFN:
             t = scratch.get(name)
             if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError(f"scratch must hold {name} {list(shape)} {dtype}")
-        self.scratch = scratch
+        # the backward of a layer that keeps everything reads these rows: no other layer may write them
+        self.scratch = scratch if save8 or not backward else None
         self.Xp, self.Ygu, self.A, self.Zp = (scratch[name] for name in ("Xp", "Ygu", "A", "Zp"))
         self.W_gu_home = torch.zeros((E, H, 2 * Hp), **act)
         self.W_gu_slots = torch.zeros((R, B, H, 2 * Hp), **act)
