@@ -207,8 +207,9 @@ class MoeFFN:
             scratch = {name: torch.empty(shape, **act) for name, shape in rows.items()}
         for name, shape in rows.items():
             t = scratch.get(name)
-            if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError(f"scratch must hold {name} {list(shape)} {dtype}")
+            if (t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()
+                    or t.device != self.X.device):
+                raise ValueError(f"scratch must hold {name} {list(shape)} {dtype} on {self.X.device}")
         # the backward of a layer that keeps everything reads these rows: no other layer may write them
         self.scratch = scratch if save8 or not backward else None
         self.Xp, self.Ygu, self.A, self.Zp = (scratch[name] for name in ("Xp", "Ygu", "A", "Zp"))

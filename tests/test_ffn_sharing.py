@@ -25,3 +25,11 @@ def test_layers_without_a_backward_share():
     a = make()
     b = make(scratch=a.scratch)
     assert b.Ygu.data_ptr() == a.Ygu.data_ptr()
+
+
+def test_rows_on_another_device_are_refused():
+    a = make(backward=True, save8=True)
+    for name in a.scratch:
+        other = {k: torch.empty_like(v, device="meta") if k == name else v for k, v in a.scratch.items()}
+        with pytest.raises(ValueError, match=f"scratch must hold {name} .*on cpu"):
+            make(backward=True, save8=True, scratch=other)
