@@ -475,7 +475,12 @@ def moonep_layernorm_backward_workspace_bytes(d: Dims, H: int) -> int:
 def _layernorm_backward(entry, d, H, code, dY, z, rstd, gamma, dX, dgamma, dbeta, workspace, stream):
     T, f32 = d.R * d.S, torch.float32
     if workspace is not None:
-        needed = moonep_layernorm_backward_workspace_bytes(d, H)
+        at = workspace.get_device()
+        if at < 0 or at == torch._C._cuda_getDevice():
+            needed = moonep_layernorm_backward_workspace_bytes(d, H)
+        else:  # the launch, whose size sets the workspace's, is for the tensors' device
+            with torch.cuda.device(at):
+                needed = moonep_layernorm_backward_workspace_bytes(d, H)
         if workspace.numel() * workspace.element_size() < needed:
             raise ValueError(f"workspace too small: {needed} bytes needed")
     _launch(entry, d, int(H), *code, (dY, "dY", f32, T * H), *z, (rstd, "rstd", f32, T), (gamma, "gamma", f32, H),

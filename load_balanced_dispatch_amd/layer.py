@@ -241,8 +241,9 @@ class MoeFFN:
                 self.dXn = torch.empty((R, S, H), **f32)
                 self.dgamma = torch.zeros(H, **f32)
                 self.dbeta = torch.zeros(H, **f32)
-                self.ws_norm = torch.empty(max(1, _lib.moonep_layernorm_backward_workspace_bytes(d, H)),
-                                           dtype=torch.uint8, device=device)
+                with torch.cuda.device(self.X.get_device()):  # its size is for the current device
+                    nbytes = _lib.moonep_layernorm_backward_workspace_bytes(d, H)
+                self.ws_norm = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
             self.dW_gu_home = torch.zeros((E, H, 2 * Hp), **f32)
             self.dW_gu_slots = torch.zeros((R, B, H, 2 * Hp), **f32)
             self.dW_down_home = torch.zeros((E, Hp, H), **f32)

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import load_balanced_dispatch_amd as m
+from load_balanced_dispatch_amd import _lib
 
 DIMS = (2, 4, 1, 6, 2, 64, 32)
 
@@ -33,3 +34,69 @@ def test_rows_on_another_device_are_refused():
         other = {k: torch.empty_like(v, device="meta") if k == name else v for k, v in a.scratch.items()}
         with pytest.raises(ValueError, match=f"scratch must hold {name} .*on cpu"):
             make(backward=True, save8=True, scratch=other)
+
+
+class FakeDevices:
+    """Stands for two GPUs whose launches differ in size: what the binding asks of torch and of the library."""
+
+    def __init__(self, monkeypatch, sizes):
+        self.current, self.sizes = 0, sizes
+        outer = self
+
+        class on:
+            def __init__(self, device):
+                self.to = torch.device(device).index if not isinstance(device, int) else device
+
+            def __enter__(self):
+                self.back, outer.current = outer.current, self.to
+
+            def __exit__(self, *exc):
+                outer.current = self.back
+
+        class Library:
+            moonep_layernorm_backward_workspace_bytes = staticmethod(lambda d, H: sizes[outer.current])
+            moonep_layernorm_backward8 = moonep_layernorm_backward = None
+
+        monkeypatch.setattr(torch.cuda, "device", on)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.current)
+        monkeypatch.setattr(_lib, "_LIB", Library)
+
+
+class FakeBytes:
+    """A uint8 tensor of n bytes on a device."""
+
+    def __init__(self, n, device):
+        self.n, self.device = n, device
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 1
+
+    def get_device(self):
+        return self.device
+
+
+def test_the_workspace_is_sized_by_its_own_device(monkeypatch):
+    # 100 bytes are enough on the current device, not on the one that the tensors are on and the launch goes to
+    gpus = FakeDevices(monkeypatch, [64, 4096])
+    d = m.make_dims(2, 4, 1, 6, 2)
+    f32 = torch.zeros(1)
+    for call in (lambda ws: m.moonep_layernorm_backward8(d, 64, f32, f32, f32, f32, f32, f32, f32, None, ws),
+                 lambda ws: m.moonep_layernorm_backward(d, 64, f32, f32, f32, f32, f32, f32, f32, None, ws)):
+        with pytest.raises(ValueError, match="workspace too small: 4096 bytes"):
+            call(FakeBytes(100, 1))
+        with pytest.raises(ValueError, match="dY must be a device tensor"):  # the size is enough: the next check
+            call(FakeBytes(4096, 1))
+        with pytest.raises(ValueError, match="dY must be a device tensor"):
+            call(FakeBytes(100, 0))
+    assert gpus.current == 0
+
+
+def test_a_layers_workspace_is_sized_by_its_device(monkeypatch):
+    FakeDevices(monkeypatch, {0: 64, -1: 4096})  # the layer is on the host, which counts as device -1
+    monkeypatch.setattr(_lib, "moonep_plan_workspace_bytes", lambda d: 1)
+    monkeypatch.setattr(_lib, "moonep_group_gemm_workspace_bytes", lambda d: 1)
+    monkeypatch.setattr(_lib, "moonep_wgrad_workspace_bytes", lambda d: 1)
+    assert make(backward=True, norm=True).ws_norm.numel() == 4096
