@@ -340,9 +340,13 @@ class MoeFFN:
         return calls
 
     def forward(self):
-        for _, f in self.forward_calls():
-            f()
+        self._run(self.forward_calls())
 
     def backward(self):
-        for _, f in self.backward_calls():
-            f()
+        self._run(self.backward_calls())
+
+    def _run(self, calls):
+        # some calls are enqueued on the current device's stream, some on their tensors': one stream if that is current
+        with torch.cuda.device(self.X.get_device()):
+            for _, f in calls:
+                f()

@@ -100,3 +100,16 @@ def test_a_layers_workspace_is_sized_by_its_device(monkeypatch):
     monkeypatch.setattr(_lib, "moonep_group_gemm_workspace_bytes", lambda d: 1)
     monkeypatch.setattr(_lib, "moonep_wgrad_workspace_bytes", lambda d: 1)
     assert make(backward=True, norm=True).ws_norm.numel() == 4096
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(norm=True), dict(norm=True, save8=True)])
+def test_a_layers_passes_run_on_its_device(monkeypatch, kw):
+    # some of the calls go to the current device's stream and some to their tensors': both are the layer's
+    L = make(backward=True, **kw)
+    gpus = FakeDevices(monkeypatch, [64, 4096])
+    L.X = FakeBytes(1, 1)
+    seen = []
+    L.forward_calls = L.backward_calls = lambda: [("step", lambda: seen.append(gpus.current))] * 2
+    L.forward()
+    L.backward()
+    assert seen == [1] * 4 and gpus.current == 0
