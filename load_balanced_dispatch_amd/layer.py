@@ -161,11 +161,12 @@ class MoeFFN:
     rows that the experts read (normalised rows with norm=True, else X) in x_codes, x_exps [R, S, ...] and the
     activation's input Ygu in ygu_codes, ygu_exps.  The row buffers of the forward pass are then free once it
     is over: they are in the dict `scratch`, which layers of one shape can share by passing one's to the
-    others' constructor (layers sharing it run one after another, as on one stream).  A layer without a backward
-    has such a dict too; with backward=True and save8=False `scratch` is None.  backward() applies the
-    gates on the experts' side: ungated output-gradient rows -> dgrad of the down projection -> swiglu backward
-    from 8 bits (which also gives the gated activation and dgates) -> wgrad of the down projection -> dispatch
-    from 8 bits -> dgrad and wgrad of the gate|up projection -> dispatch backward -> reduce_grad.
+    others' constructor (layers sharing it run one after another, as on one stream); with norm=True dXn, which is
+    used inside backward() only, is there as well.  A layer without a backward has such a dict too; with
+    backward=True and save8=False `scratch` is None.  backward() applies the gates on the experts' side: ungated
+    output-gradient rows -> dgrad of the down projection -> swiglu backward from 8 bits (which also gives the gated
+    activation and dgates) -> wgrad of the down projection -> dispatch from 8 bits -> dgrad and wgrad of the
+    gate|up projection -> dispatch backward -> reduce_grad.
     """
 
     def __init__(self, R, E, B, S, K, H, Hp, dtype=torch.bfloat16, device="cuda", backward=False, norm=False,
@@ -238,7 +239,13 @@ class MoeFFN:
                 self.dXp = torch.empty((N, H), **act)
             self.dX = torch.empty((R, S, H), **f32)
             if norm:
-                self.dXn = torch.empty((R, S, H), **f32)
+                # inside one backward pass only, so save8's layers of the same tokens share it with their rows
+                kind = lambda t: (t.shape, t.dtype, t.device, t.is_contiguous())  # noqa: E731
+                self.dXn = scratch.get("dXn") if save8 else None
+                if self.dXn is None or kind(self.dXn) != kind(self.dX):
+                    self.dXn = torch.empty((R, S, H), **f32)
+                    if save8:
+                        scratch.setdefault("dXn", self.dXn)
                 self.dgamma = torch.zeros(H, **f32)
                 self.dbeta = torch.zeros(H, **f32)
                 with torch.cuda.device(self.X.get_device()):  # its size is for the current device

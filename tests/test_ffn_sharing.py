@@ -113,3 +113,22 @@ def test_a_layers_passes_run_on_its_device(monkeypatch, kw):
     L.forward()
     L.backward()
     assert seen == [1] * 4 and gpus.current == 0
+
+
+def test_the_gradient_of_the_norms_rows_is_shared_too():
+    # it lives inside one backward pass only, like the row buffers
+    a = make(backward=True, norm=True, save8=True)
+    b = make(backward=True, norm=True, save8=True, scratch=a.scratch)
+    assert b.dXn.data_ptr() == a.dXn.data_ptr() and b.dX.data_ptr() != a.dX.data_ptr()
+    assert a.dXn.shape == a.dX.shape and a.dXn.dtype == torch.float32
+    # buffers from a layer without a norm get one with the first layer that has
+    c = make(backward=True, save8=True)
+    assert "dXn" not in c.scratch
+    d, e = (make(backward=True, norm=True, save8=True, scratch=c.scratch) for _ in range(2))
+    assert d.Xp.data_ptr() == c.Xp.data_ptr() and e.dXn.data_ptr() == d.dXn.data_ptr()
+    # the same rows of other tokens (12 of one pair each for 6 of two): its own, the others' stays
+    f = m.MoeFFN(2, 4, 1, 12, 1, 64, 32, device="cpu", backward=True, norm=True, save8=True, scratch=a.scratch)
+    assert f.Xp.data_ptr() == a.Xp.data_ptr() and f.dXn.shape == f.dX.shape
+    assert a.scratch["dXn"].data_ptr() == a.dXn.data_ptr() != f.dXn.data_ptr()
+    # a layer that keeps everything has its own
+    assert make(backward=True, norm=True).dXn.shape == a.dXn.shape
