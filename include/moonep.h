@@ -323,7 +323,7 @@ int moonep_reduce_grad(moonep_dims d, int32_t H, int32_t Hp, const int32_t* slot
  *   b = max(1, biased float32 exponent of its largest magnitude),  step = 2^(b - 133),
  *   code = x / step rounded to the nearest even whole number, held within +-127;  value = code * step.
  * A value is off by at most step / 2 (by step where |x| is within step / 2 of 128 steps), and step is at
- * most 1/64 of the block's largest magnitude.  x / step and code * step are exact, and every value is a
+ * most 1/64 of the block's largest magnitude (2^-132 where that is below 2^-126).  x / step and code * step are exact, and every value is a
  * bfloat16 number.  A block with an infinity or a NaN has b = 255: all its values are NaN, its codes
  * unspecified.
  *

@@ -6,7 +6,7 @@
 //   dgamma += sum over rows of dy z,  dbeta += sum over rows of dy
 // The forward can write z in 8 bits (save8.hpp) in the same pass; the backward then reads that instead
 // of x, and moonep_dispatch8 makes the expert inputs from it again.  moonep_layernorm_dispatch writes y straight
-// to its pairs' places (32 768 rows of 2048 columns to 6 places each: 200 us, 239 as two calls).
+// to its pairs' places (32 768 rows of 2048 columns to 6 places each, with a checkpoint: 201 us, 237 as two calls).
 //
 // A row is read from HBM once and held in registers by one wave or by all waves of a block; sums run over
 // lanes with DPP moves, over waves through LDS, always in the same order.
@@ -608,7 +608,8 @@ void layernorm_launch(const RowShape& q, int64_t rows, int H, const void* X, con
 
 // Up to this many rows the one launch is faster at every width (512 rows, measured on the GPU alone: 4.8 us
 // against 6.6 at 128 columns, 7.7 against 10.0 at 2048, 14.6 against 15.6 at 7168; 256 rows of 2048: 5.5
-// against 9.0); with 1024 rows the two are at 1024 columns and more (10.1 us against 11.3, 20.5 against 26.0 at 7168).
+// against 9.0); with 1024 rows the two launches are faster at 1024 columns and more (10.1 us against 11.3, 20.5 against
+// 26.0 at 7168).
 constexpr int kFewRows = 512;
 // Widths to which a wave per row is faster there than a block (256 rows: 6.5 us against 7.5 at 1024 columns, but 4.7
 // against 3.5 for 16 rows).

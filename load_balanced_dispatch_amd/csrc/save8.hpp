@@ -4,7 +4,8 @@
 // columns let b = max(1, the biased exponent of the largest magnitude as float32); the block's step is
 // 2^(b - 133) and a code is the value over the step, rounded to even and held within +-127.  The
 // largest magnitude over the step lies in [64, 128), so a value is off by at most half a step (a step
-// where it lies within half a step of 128), and the step is at most 1/64 of the largest magnitude.
+// where it lies within half a step of 128), and the step is at most 1/64 of the largest magnitude
+// (the largest magnitude a normal number; below 2^-126 the step is 2^-132).
 //
 // The step is a power of two so that nothing but the one rounding to a code is ever lost: value / step
 // and code * step are exact in float32, code * step is a bf16 number (7 bits and a sign), and the
@@ -15,9 +16,9 @@
 // step that overflowed is seen by the backward pass as it would be with the values kept whole.
 //
 // Kernels give a lane 8 columns (16 bytes of bf16; the norm's backward, whose rows are float32, 4) and a
-// block a quad of lanes, so the block's largest magnitude takes two DPP moves.  Each kernel is built twice: AL for rows whose 8-column chunks are
-// whole and aligned, and without for any width and alignment, with the same wide accesses at element
-// alignment and a last chunk element by element.
+// block a quad of lanes, so the block's largest magnitude takes two DPP moves.  Each kernel is built twice: AL for
+// rows whose 8-column chunks are whole and aligned, and without for any width and alignment, with the same wide
+// accesses at element alignment and a last chunk element by element.
 #pragma once
 
 #include "moonep_common.h"
@@ -223,9 +224,11 @@ __device__ __forceinline__ void decode(u32x2 q, float step, float (&f)[kChunk]) 
 // ------------------------------------------------------------------ host side
 
 // Whether rows of type T, `bytes` of them, are written past the caches (PAST).  The call that follows reads them, from
-// the 256 MB last-level cache where they still are there: norm and dispatch of 32 768 x 2048 (134 MB) took 237 us
-// with ordinary stores of the norm's rows and 243 with non-temporal ones, of 32 768 x 7168 (470 MB) 1043 and
-// 1028; alone, the kernels here run 4-15% faster with non-temporal stores.
+// the 256 MB last-level cache where they still are there: moonep_layernorm followed by moonep_dispatch of
+// 32 768 x 2048 (134 MB) took 237 us with ordinary stores of the norm's rows and 243 with non-temporal ones, of
+// 32 768 x 7168 (470 MB) 1043 and 1028; alone, the kernels that store a row once, and dispatch from 8 bits, run 4-15%
+// faster with non-temporal stores.  moonep_dispatch stores ordinarily up to 4 GiB, which was faster there; which is
+// faster for moonep_layernorm_dispatch, which goes by the rule here, has not been measured.
 template <typename T>
 bool past_caches(bool al, int64_t bytes) {
   return al && sizeof(T) == 2 && bytes > (int64_t(256) << 20);

@@ -155,7 +155,8 @@ class MoeFFN:
 
     `norm=True` puts a layer norm (gamma, beta [H] float32, eps) in front: X is then its input, dispatch lays
     out its rows in the same pass, and backward() continues through it from their gradient dXn to dX, adding into
-    dgamma and dbeta.
+    dgamma and dbeta.  The norm's backward reads X again unless save8=True, so X must keep its values until then
+    (without a norm a program may overwrite X once forward() is over).
 
     `save8=True` (with backward=True) keeps only 8 bits of two activations from forward() to backward(): the
     rows that the experts read (normalised rows with norm=True, else X) in x_codes, x_exps [R, S, ...] and the

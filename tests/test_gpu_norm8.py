@@ -295,7 +295,8 @@ def test_combine_backward_ungated(m, dtype, D, K):
 
 # ------------------------------------------------------------------ layer norm
 
-# a wave per row with 1, 2 and 4 chunks a lane; a block per row with 2 and 4; odd widths of each
+# forward: a wave per row with 1 and 2 chunks a lane, a block per row with 1 (three waves), 2 and 4; backward: a wave per
+# row with 1, 2 and 4, groups of waves, a block per row with 2, 4 and 8; odd widths among them
 NORM_WIDTHS = [1, 2, 7, 8, 33, 128, 253, 512, 513, 1000, 1024, 1413, 2048, 2056, 2500, 7168, 16384, 16392, 20001,
                32768]
 
