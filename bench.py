@@ -18,6 +18,8 @@ dgrad, dispatch backward) as `next_rows`, the sweep and its flatness, the other
 workloads timed after the headline one (`other_workloads`: the mid sweep with
 the backward workload's point, the mid gated FFN, the routing-stress
 plan + dispatch), and the CPU oracle's plan + dispatch rate on a bounded sample.
+To keep the line short, `other_workloads`, `planners` (copies of both) and
+`sweep_mincopy_planner` go to stderr as one JSON object, "[bench] details {...}".
 
     python bench.py --stats-md run_kernel_stats.csv          (rocprofv3 summary -> markdown)
     python bench.py --traffic-md fetch.csv write.csv         (counter runs -> per-stage HBM bytes)
@@ -1040,6 +1042,17 @@ def planner_table(args, alpha_of, reps=10):
     return out
 
 
+# Sections that do not go on the line: with them it is over 20 KB, and a reader that keeps the last 10 KB or so of
+# the output loses its front, where the headline is.
+DETAILS = ("sweep_mincopy_planner", "planners", "other_workloads")
+
+
+def split_record(record):
+    """The record's line, and the sections that are reported beside it (those that were measured)."""
+    details = {k: record[k] for k in DETAILS if record.get(k) is not None}
+    return {k: v for k, v in record.items() if k not in DETAILS}, details
+
+
 def main():
     args = parse()
     if args.gpus != 1:
@@ -1259,7 +1272,10 @@ def main():
         "planners": planners,
         "other_workloads": extras,
     }
-    print(json.dumps(line), flush=True)
+    line, details = split_record(line)
+    if details:
+        log("details", json.dumps(details))
+    print(json.dumps(line, separators=(",", ":")), flush=True)
 
 
 if __name__ == "__main__":
