@@ -400,7 +400,8 @@ int moonep_combine_backward_ungated(moonep_dims d, int32_t D, moonep_dtype t, co
 
 /*
  * moonep_layernorm -- with m and v the mean and variance (divided by H) of a row x, r = 1 / sqrt(v + eps) and
- *   z = (x - m) * r:  Y = z * gamma + beta;  float32 arithmetic, rounded once to dtype t.
+ *   z = (x - m) * r:  Y = z * gamma + beta;  float32 arithmetic, rounded once to dtype t.  Rows are not scaled first:
+ *   where their sum passes float32's range Y is NaN, where the sum of (x - m)^2 does r is 0 and Y is beta.
  * In:  X [R,S,H] dtype t;  gamma [H] float32;  beta [H] float32 or NULL (0);  eps > 0.
  * Out: Y [R,S,H] dtype t;  mean [R,S] (m), rstd [R,S] (r) float32, each NULL to skip;
  *      codes [R,S,H] int8, exps [R,S,moonep_save8_blocks(H)] uint8: z in 8 bits, both NULL to skip.
