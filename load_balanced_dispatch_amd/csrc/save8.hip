@@ -77,9 +77,9 @@ __global__ __launch_bounds__(load8_threads(AL)) void load8_rows(const int8_t* __
 // ------------------------------------------------------------------ activation
 
 // 1 / x for x in [1, 2]: the hardware's reciprocal and a Newton step, without the general division's handling of
-// other ranges.  It gives the correctly rounded quotient: the tests compare the activation built on it with the plain
-// one, which divides, over nearly all those x.  The activation with its checkpoint took 365 us so, 388 with the division
-// (196 608 x 1408).
+// other ranges.  It gives the correctly rounded quotient: the tests compare the activation built on it with the
+// plain one, which divides, over nearly all those x.  The activation with its checkpoint took 365 us so, 388 with
+// the division (196 608 x 1408).
 __device__ __forceinline__ float recip_1_2(float x) {
   const float r = __builtin_amdgcn_rcpf(x);
   return __builtin_fmaf(__builtin_fmaf(-x, r, 1.f), r, r);
