@@ -442,6 +442,116 @@ int moonep_layernorm_backward8(moonep_dims d, int32_t H, const float* dY, const 
                                const float* rstd, const float* gamma, float* dX, float* dgamma, float* dbeta,
                                void* workspace, moonep_stream stream);
 
+/*
+ * Router: from scores to the chosen experts and their gates, and back.  The pages' path starts from a router's top-K
+ * output ([P2] "Core problem") and does not describe the router; these calls make topk_idx and gates from the logits
+ * that a program's router projection gives, and carry dgates back to them.
+ */
+
+/* Router scores of a token's logits l. */
+typedef enum moonep_score {
+  MOONEP_SCORE_SOFTMAX = 0, /* s_e = exp(l_e) / sum over all experts of exp(l) */
+  MOONEP_SCORE_SIGMOID = 1  /* s_e = 1 / (1 + exp(-l_e)) */
+} moonep_score;
+
+/*
+ * moonep_route -- the K experts of every token and their gates.
+ *   The experts are the K largest of l_e, or with a bias of s_e + bias_e (in float64, which changes the choice only),
+ *   in descending order, the lowest id first among equals.
+ *   gates = scale * s_e, or with renorm scale * s_e / (sum of the chosen experts' s); float32 arithmetic.
+ *   A logit of NaN or -inf masks its expert: it has s = 0 and is never chosen, as one whose bias is NaN or -inf is not
+ *   chosen.  +inf counts as the largest float.  A token with fewer than K experts to choose from has id -1 (which the
+ *   other calls leave out) and gate 0 in the places that are left.
+ * In:  logits [R,S,E] float32;  bias [E] float32 or NULL.
+ * Out: topk_idx [R,S,K] int32;  gates [R,S,K] float32.
+ * E <= 4096; B is not used.
+ */
+int moonep_route(moonep_dims d, int32_t score, int32_t renorm, float scale, const float* logits, const float* bias,
+                 int32_t* topk_idx, float* gates, moonep_stream stream);
+
+/*
+ * moonep_route_backward -- the gradient of moonep_route's gates with respect to the logits (the choice and the bias have
+ *   none), with c_k = scale * dgates_k and, with renorm, q_k = s_k / (sum of the chosen s), u_k = c_k - sum_j q_j c_j:
+ *     softmax          dl_e = s_e * (c_k where e is chosen, 0 elsewhere) - s_e * sum_j s_j c_j
+ *     sigmoid          dl_e = c_k * s_e * (1 - s_e) where e is chosen, 0 elsewhere
+ *     softmax, renorm  dl_e = q_k * u_k             where e is chosen, 0 elsewhere
+ *     sigmoid, renorm  dl_e = q_k * u_k * (1 - s_e) where e is chosen, 0 elsewhere
+ *   float32 arithmetic.  Ids outside [0, E) are left out; a masked expert's gradient is 0.  The gradients of an id
+ *   that a token holds more than once add up.
+ * In:  logits [R,S,E] float32;  topk_idx [R,S,K] int32 as moonep_route gives it;  dgates [R,S,K] float32.
+ * Out: dlogits [R,S,E] float32 (all of it is written).
+ */
+int moonep_route_backward(moonep_dims d, int32_t score, int32_t renorm, float scale, const float* logits,
+                          const int32_t* topk_idx, const float* dgates, float* dlogits, moonep_stream stream);
+
+/*
+ * The layer for few tokens (decoding).  With a handful of tokens the time goes into reading the chosen experts'
+ * weights, and a plan, slots and row buffers have nothing to balance: these calls take topk_idx and gates as they are,
+ * read each chosen expert's home weights once and need no plan.  They take R*S*K <= MOONEP_FEW_PAIRS pairs
+ * (MOONEP_EINVAL beyond: the planned calls are for those), H and Hp up to 65536, and use of d only R, E, S and K.
+ * Products and sums are float32 and nothing is rounded to dtype t on the way.  Pairs whose id is outside [0, E) are
+ * left out.  Results are the same from call to call.
+ */
+enum { MOONEP_FEW_PAIRS = 1024 };
+
+/* Bytes of device workspace the calls below need for projections of these widths (256-byte aligned pointer; calls that
+ * can overlap need one each; contents ignored on entry). */
+size_t moonep_few_workspace_bytes(moonep_dims d, int32_t H, int32_t Hp);
+
+/*
+ * moonep_few_layer -- one expert projection and the combine:
+ *   out[r,s] = sum over k ascending of gates[r,s,k] * (X[r,s] @ W_home[topk_idx[r,s,k]]).
+ * In:  X [R,S,H] dtype t;  topk_idx [R,S,K] int32;  gates [R,S,K] float32 or NULL (1);  W_home [E,H,Hp] dtype t.
+ * Out: out [R,S,Hp] float32.
+ */
+int moonep_few_layer(moonep_dims d, int32_t H, int32_t Hp, moonep_dtype t, const void* X, const int32_t* topk_idx,
+                     const float* gates, const void* W_home, float* out, void* workspace, moonep_stream stream);
+
+/*
+ * moonep_few_ffn -- the whole gated expert layer:
+ *   out[r,s] = sum over k ascending of gates[r,s,k] * (A @ W_down[e]),  e = topk_idx[r,s,k],
+ *   A = silu(X[r,s] @ W_gu[e][:, :Hp]) * (X[r,s] @ W_gu[e][:, Hp:]).
+ * In:  X [R,S,H] dtype t;  topk_idx [R,S,K] int32;  gates [R,S,K] float32 or NULL (1);
+ *      W_gu [E,H,2*Hp], W_down [E,Hp,H] dtype t.
+ * Out: out [R,S,H] float32.
+ */
+int moonep_few_ffn(moonep_dims d, int32_t H, int32_t Hp, moonep_dtype t, const void* X, const int32_t* topk_idx,
+                   const float* gates, const void* W_gu, const void* W_down, float* out, void* workspace,
+                   moonep_stream stream);
+
+/*
+ * Weights in 4 bits.  A weight tensor [E, H, N] is kept as codes in [-8, 7] and one bfloat16 scale per column and G input
+ * rows (G = 32, 64 or 128; the last group covers what is left of H):  value = code * scale.
+ *   codes  [E, ceil(H/8), N] int32: the word of rows 8j .. 8j+7 of a column holds the code of row 8j+i, plus 8, in the
+ *          four bits from 4*(i/2) + 16*(i%2) on.  Codes of rows past H are written as 0 and read as nothing.
+ *   scales [E, ceil(H/G), N] bfloat16 (as 16 bits).
+ */
+
+/*
+ * moonep_save4 -- weights into 4 bits: scale = (largest magnitude of the group) / 7, rounded to bfloat16;
+ *   code = value / scale rounded to the nearest even whole number, held within [-8, 7] (0 where the scale is 0).
+ *   A group with an infinity or a NaN has the scale NaN.
+ * moonep_load4 -- the values that 4-bit weights stand for (float32: exactly; bf16: rounded once).
+ * In/Out: W [E,H,N] dtype t;  codes, scales as above.  E >= 0; H, N up to 65536.
+ */
+int moonep_save4(int32_t E, int32_t H, int32_t N, int32_t G, moonep_dtype t, const void* W, int32_t* codes,
+                 uint16_t* scales, moonep_stream stream);
+int moonep_load4(int32_t E, int32_t H, int32_t N, int32_t G, moonep_dtype t, const int32_t* codes,
+                 const uint16_t* scales, void* W, moonep_stream stream);
+
+/*
+ * moonep_few_layer4, moonep_few_ffn4 -- moonep_few_layer and moonep_few_ffn with weights in 4 bits (W_gu [E,H,2*Hp],
+ *   W_down [E,Hp,H], both with groups of G rows).  With E = K = 1 and no gates moonep_few_layer4 is the product of few
+ *   rows with one 4-bit matrix.  dtype t is X's.  Input magnitudes up to 2^110 (infinities give NaN).
+ */
+int moonep_few_layer4(moonep_dims d, int32_t H, int32_t Hp, int32_t G, moonep_dtype t, const void* X,
+                      const int32_t* topk_idx, const float* gates, const int32_t* codes, const uint16_t* scales,
+                      float* out, void* workspace, moonep_stream stream);
+int moonep_few_ffn4(moonep_dims d, int32_t H, int32_t Hp, int32_t G, moonep_dtype t, const void* X,
+                    const int32_t* topk_idx, const float* gates, const int32_t* gu_codes, const uint16_t* gu_scales,
+                    const int32_t* down_codes, const uint16_t* down_scales, float* out, void* workspace,
+                    moonep_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

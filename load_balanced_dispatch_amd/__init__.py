@@ -11,7 +11,10 @@ moonep_layernorm, moonep_layernorm_dispatch, moonep_layernorm_backward,
 moonep_layernorm_backward8 -- and
 the 8-bit activation checkpoints -- moonep_save8, moonep_load8,
 moonep_swiglu_save8, moonep_swiglu_backward8, moonep_dispatch8,
-moonep_combine_backward_ungated -- exposed here under the same names, taking
+moonep_combine_backward_ungated -- the router -- moonep_route,
+moonep_route_backward -- and the layer for few tokens, its weights in 16 or 4
+bits -- moonep_few_layer, moonep_few_ffn, moonep_few_layer4, moonep_few_ffn4,
+moonep_save4, moonep_load4 -- exposed here under the same names, taking
 torch tensors.  Importing this
 package loads libmoonep.so and raises if it is missing; there is no CPU or
 PyTorch fallback.
@@ -28,6 +31,9 @@ from ._lib import (  # noqa: F401
     moonep_combine_backward_ungated, moonep_layernorm, moonep_layernorm_dispatch,
     moonep_layernorm_backward_workspace_bytes,
     moonep_layernorm_backward, moonep_layernorm_backward8,
+    MOONEP_SCORE_SOFTMAX, MOONEP_SCORE_SIGMOID, SCORES, MOONEP_FEW_PAIRS, moonep_route, moonep_route_backward,
+    moonep_few_workspace_bytes, moonep_few_layer, moonep_few_ffn, moonep_few_layer4, moonep_few_ffn4, moonep_save4,
+    moonep_load4,
 )
 from .layer import MoeFFN  # noqa: F401
 from .layer import MoeLayer  # noqa: F401

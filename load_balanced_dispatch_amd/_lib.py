@@ -19,6 +19,9 @@ LIB_PATH = os.path.join(HERE, "libmoonep.so")
 
 MOONEP_F32, MOONEP_BF16 = 0, 1
 MOONEP_PLAN_PREFIX, MOONEP_PLAN_MINCOPY = 0, 1
+MOONEP_SCORE_SOFTMAX, MOONEP_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOONEP_SCORE_SOFTMAX, "sigmoid": MOONEP_SCORE_SIGMOID}
+MOONEP_FEW_PAIRS = 1024
 PLANNERS = {"prefix": MOONEP_PLAN_PREFIX, "mincopy": MOONEP_PLAN_MINCOPY}
 MOONEP_OK, MOONEP_EINVAL, MOONEP_EHIP, MOONEP_EUNSUPPORTED = 0, -1, -2, -3
 _CODES = {MOONEP_EINVAL: "EINVAL", MOONEP_EHIP: "EHIP", MOONEP_EUNSUPPORTED: "EUNSUPPORTED"}
@@ -87,6 +90,15 @@ def _load():
         "moonep_layernorm_backward_workspace_bytes": (sz, [Dims, i32]),
         "moonep_layernorm_backward": (ctypes.c_int, [Dims, i32, ctypes.c_int] + [vp] * 10),
         "moonep_layernorm_backward8": (ctypes.c_int, [Dims, i32] + [vp] * 10),
+        "moonep_route": (ctypes.c_int, [Dims, i32, i32, ctypes.c_float] + [vp] * 5),
+        "moonep_route_backward": (ctypes.c_int, [Dims, i32, i32, ctypes.c_float] + [vp] * 5),
+        "moonep_few_workspace_bytes": (sz, [Dims, i32, i32]),
+        "moonep_few_layer": (ctypes.c_int, [Dims, i32, i32, ctypes.c_int] + [vp] * 7),
+        "moonep_few_ffn": (ctypes.c_int, [Dims, i32, i32, ctypes.c_int] + [vp] * 8),
+        "moonep_save4": (ctypes.c_int, [i32, i32, i32, i32, ctypes.c_int] + [vp] * 4),
+        "moonep_load4": (ctypes.c_int, [i32, i32, i32, i32, ctypes.c_int] + [vp] * 4),
+        "moonep_few_layer4": (ctypes.c_int, [Dims, i32, i32, i32, ctypes.c_int] + [vp] * 8),
+        "moonep_few_ffn4": (ctypes.c_int, [Dims, i32, i32, i32, ctypes.c_int] + [vp] * 10),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -105,7 +117,9 @@ SYMBOLS = ("moonep_last_error", "moonep_plan_workspace_bytes", "moonep_plan", "m
            "moonep_group_gemm_dgrad", "moonep_dispatch_backward", "moonep_swiglu", "moonep_swiglu_backward",
            "moonep_save8_blocks", "moonep_save8", "moonep_load8", "moonep_swiglu_save8", "moonep_swiglu_backward8",
            "moonep_dispatch8", "moonep_combine_backward_ungated", "moonep_layernorm", "moonep_layernorm_dispatch",
-           "moonep_layernorm_backward_workspace_bytes", "moonep_layernorm_backward", "moonep_layernorm_backward8")
+           "moonep_layernorm_backward_workspace_bytes", "moonep_layernorm_backward", "moonep_layernorm_backward8",
+           "moonep_route", "moonep_route_backward", "moonep_few_workspace_bytes", "moonep_few_layer",
+           "moonep_few_ffn", "moonep_save4", "moonep_load4", "moonep_few_layer4", "moonep_few_ffn4")
 
 
 def lib():
@@ -502,3 +516,93 @@ def moonep_layernorm_backward8(d: Dims, H: int, dY, codes, exps, rstd, gamma, dX
     """moonep_layernorm_backward from the 8-bit normalised rows."""
     _layernorm_backward(_LIB.moonep_layernorm_backward8, d, H, (), dY, _rows8(codes, exps, d.R * d.S, H), rstd, gamma,
                         dX, dgamma, dbeta, workspace, stream)
+
+
+# ------------------------------------------------------------------ router, layer for few tokens, 4-bit weights
+
+def _score_code(score) -> int:
+    if isinstance(score, str):
+        if score not in SCORES:
+            raise ValueError(f"unknown score {score!r}; one of {sorted(SCORES)}")
+        return SCORES[score]
+    return int(score)
+
+
+def moonep_route(d: Dims, score, renorm: bool, scale: float, logits, bias, topk_idx, gates, stream=None):
+    """The K experts of every token of logits [R,S,E], and their gates: score "softmax" or "sigmoid"; bias (float32 [E]
+    or None) corrects the choice only."""
+    f32 = torch.float32
+    _launch(_LIB.moonep_route, d, _score_code(score), int(bool(renorm)), float(scale),
+            (logits, "logits", f32, d.R * d.S * d.E), _or_none(bias, "bias", f32, d.E),
+            (topk_idx, "topk_idx", torch.int32, d.N), (gates, "gates", f32, d.N), stream=stream)
+
+
+def moonep_route_backward(d: Dims, score, renorm: bool, scale: float, logits, topk_idx, dgates, dlogits, stream=None):
+    """Gradient of moonep_route's gates: writes dlogits [R,S,E] from dgates [R,S,K]."""
+    f32 = torch.float32
+    n = d.R * d.S * d.E
+    _launch(_LIB.moonep_route_backward, d, _score_code(score), int(bool(renorm)), float(scale),
+            (logits, "logits", f32, n), (topk_idx, "topk_idx", torch.int32, d.N), (dgates, "dgates", f32, d.N),
+            (dlogits, "dlogits", f32, n), stream=stream)
+
+
+def moonep_few_workspace_bytes(d: Dims, H: int, Hp: int) -> int:
+    """Bytes of workspace of the calls for few tokens (0 for dims that they refuse)."""
+    return int(_LIB.moonep_few_workspace_bytes(d, int(H), int(Hp)))
+
+
+def _few(entry, d, H, Hp, G, X, topk_idx, gates, weights, out, wide, workspace, stream):
+    t, code = _row_type(X, "X")
+    if workspace is not None and workspace.numel() * workspace.element_size() < moonep_few_workspace_bytes(d, H, Hp):
+        raise ValueError(f"workspace too small: {moonep_few_workspace_bytes(d, H, Hp)} bytes needed")
+    T, f32 = d.R * d.S, torch.float32
+    _launch(entry, d, int(H), int(Hp), *G, code, (X, "X", t, T * H), (topk_idx, "topk_idx", torch.int32, d.N),
+            _or_none(gates, "gates", f32, d.N), *weights, (out, "out", f32, T * wide),
+            (workspace, "workspace", None, None), stream=stream)
+
+
+def _weights4(codes, scales, E, H, N, G, name):
+    """4-bit weights [E, H, N] as arguments (a refused G is left to the library)."""
+    return ((codes, name + "codes", torch.int32, E * -(-H // 8) * N),
+            (scales, name + "scales", torch.bfloat16, E * -(-H // max(1, G)) * N))
+
+
+def moonep_few_layer(d: Dims, H: int, Hp: int, X, topk_idx, gates, W_home, out, workspace, stream=None):
+    """One expert projection and the combine for few tokens, without a plan: out [R,S,Hp] float32."""
+    _few(_LIB.moonep_few_layer, d, H, Hp, (), X, topk_idx, gates,
+         ((W_home, "W_home", _row_type(X, "X")[0], d.E * H * Hp),), out, Hp, workspace, stream)
+
+
+def moonep_few_ffn(d: Dims, H: int, Hp: int, X, topk_idx, gates, W_gu, W_down, out, workspace, stream=None):
+    """The whole gated expert layer for few tokens, without a plan: out [R,S,H] float32."""
+    t = _row_type(X, "X")[0]
+    _few(_LIB.moonep_few_ffn, d, H, Hp, (), X, topk_idx, gates,
+         ((W_gu, "W_gu", t, d.E * H * 2 * Hp), (W_down, "W_down", t, d.E * Hp * H)), out, H, workspace, stream)
+
+
+def moonep_few_layer4(d: Dims, H: int, Hp: int, G: int, X, topk_idx, gates, codes, scales, out, workspace, stream=None):
+    """moonep_few_layer with 4-bit weights."""
+    _few(_LIB.moonep_few_layer4, d, H, Hp, (int(G),), X, topk_idx, gates, _weights4(codes, scales, d.E, H, Hp, G, ""),
+         out, Hp, workspace, stream)
+
+
+def moonep_few_ffn4(d: Dims, H: int, Hp: int, G: int, X, topk_idx, gates, gu_codes, gu_scales, down_codes, down_scales,
+                    out, workspace, stream=None):
+    """moonep_few_ffn with 4-bit weights."""
+    _few(_LIB.moonep_few_ffn4, d, H, Hp, (int(G),), X, topk_idx, gates,
+         _weights4(gu_codes, gu_scales, d.E, H, 2 * Hp, G, "gu_") + _weights4(down_codes, down_scales, d.E, Hp, H, G,
+                                                                               "down_"), out, H, workspace, stream)
+
+
+def moonep_save4(E: int, H: int, N: int, G: int, W, codes, scales, stream=None):
+    """Weights W [E,H,N] into 4 bits: codes int32 [E, ceil(H/8), N], scales bfloat16 [E, ceil(H/G), N]."""
+    t, code = _row_type(W, "W")
+    _launch(_LIB.moonep_save4, int(E), int(H), int(N), int(G), code, (W, "W", t, E * H * N),
+            *_weights4(codes, scales, E, H, N, G, ""), stream=stream)
+
+
+def moonep_load4(E: int, H: int, N: int, G: int, codes, scales, W, stream=None):
+    """Writes the values of 4-bit weights to W [E,H,N] (float32 exactly, bfloat16 rounded)."""
+    t, code = _row_type(W, "W")
+    _launch(_LIB.moonep_load4, int(E), int(H), int(N), int(G), code, *_weights4(codes, scales, E, H, N, G, ""),
+            (W, "W", t, E * H * N), stream=stream)

@@ -41,6 +41,8 @@ int check_dims(const moonep_dims& d, const char* who);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
 inline int64_t n_pairs(const moonep_dims& d) { return (int64_t)d.R * d.S * d.K; }
 
 inline size_t elem_bytes(moonep_dtype t) { return t == MOONEP_BF16 ? 2 : 4; }

@@ -25,10 +25,12 @@ Modules:
                and gradients, single projection and full FFN) they must reproduce.
   norm8     -- layer norm, 8-bit rows, and the gated expert FFN's backward from
                8-bit checkpoints.
+  few       -- the router and its gradient, 4-bit weights, the expert layer for
+               few tokens.
   mincopies -- brute-force minimum number of redundant copies on tiny inputs.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test
 against hand-worked examples, closed forms, invariants or brute force (see
 tests/test_oracle_*.py).  No function is parity-unpinned.
 """
-from . import planner, layer, norm8, mincopies  # noqa: F401
+from . import planner, layer, norm8, few, mincopies  # noqa: F401
