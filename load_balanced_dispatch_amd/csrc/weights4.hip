@@ -1,68 +1,207 @@
 // moonep_save4 / moonep_load4: an expert weight tensor [E, H, N] into 4 bits with a scale per column and G rows, and back.
 //
-// scale = bf16(max |w| / 7), code = w / scale rounded to even within [-8, 7]; both divisions are exactly rounded, so
+// scale = bf16(max |w| / 7), code = w / scale rounded to even within [-8, 7]; both quotients are exactly rounded, so
 // the codes are those of the formula in float32.  A group that holds an infinity or a NaN has the scale NaN.
+//
+// Both are HBM streams.  A lane takes four columns of 32 rows (whole 512-byte to 1 KB pieces of a row to a wave), a block
+// four waves one below the other: waves that share a group of 64 or 128 rows exchange its largest magnitude through LDS, so
+// that weights are read once whatever G is.
 #include "weights4.h"
 
 namespace moonep {
 namespace {
 
 constexpr int kMaxWidth = 65536;
+constexpr int kRows4 = 32, kCols4 = 4, kWaves4 = 4;  // rows and columns of a lane, waves of a block
 
-template <typename T>
-__device__ float as_float(T v) {
-  if constexpr (sizeof(T) == 2) return bf16_to_f32(v);
-  else return v;
-}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
-// A thread per column of a group.
+// Four columns of a row as bits of float32, and back; n of them are there.
 template <typename T>
-__global__ __launch_bounds__(256) void save4_columns(const T* __restrict__ W, int32_t* __restrict__ codes,
-                                                     uint16_t* __restrict__ scales, int H, int N, int G) {
-  const int groups = (H + G - 1) / G, J = (H + 7) / 8;
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  const int64_t e = blockIdx.y / groups;
-  const int g = blockIdx.y % groups;
-  if (c >= N) return;
-  const int h0 = g * G, h1 = min(H, h0 + G);
-  const T* w = W + e * H * N + c;
-  float m = 0.f;
-  bool finite = true;
-  for (int h = h0; h < h1; ++h) {
-    const float v = fabsf(as_float(w[(int64_t)h * N]));
-    finite &= v < INFINITY;
-    m = fmaxf(m, v);
-  }
-  const uint16_t s16 = finite ? f32_to_bf16(m / 7.f) : 0x7fc0;
-  scales[(e * groups + g) * N + c] = s16;
-  const float s = bf16_to_f32(s16);
-  for (int j = h0 / 8; j * 8 < h1; ++j) {
-    uint32_t word = 0;
-    for (int i = 0; i < 8; ++i) {
-      const int h = 8 * j + i;
-      float q = 0.f;
-      if (h < h1 && s > 0.f) q = fminf(fmaxf(rintf(as_float(w[(int64_t)h * N]) / s), -8.f), 7.f);
-      word |= (uint32_t)((int)q + 8) << code4_bit(i);
+struct Four;
+template <>
+struct Four<uint16_t> {
+  u32x2 q;
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= 4) {
+      q = *reinterpret_cast<const u32x2_a2*>(p);
+    } else {
+      q = (u32x2)(0u);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) q[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
     }
-    codes[(e * J + j) * N + c] = (int32_t)word;
+  }
+  __device__ __forceinline__ uint32_t bits(int i) const { return i % 2 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16; }
+  static __device__ __forceinline__ void store(uint16_t* p, const float (&v)[4], int n) {
+    if (n >= 4) {
+      *reinterpret_cast<u32x2_a2*>(p) = u32x2{f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                             f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) p[i] = f32_to_bf16(v[i]);
+    }
+  }
+};
+template <>
+struct Four<float> {
+  f32x4 q;
+  __device__ __forceinline__ void load(const float* p, int n) {
+    if (n >= 4) {
+      q = *reinterpret_cast<const f32x4_a4*>(p);
+    } else {
+      q = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) q[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ uint32_t bits(int i) const { return __float_as_uint(q[i]); }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[4], int n) {
+    if (n >= 4) {
+      *reinterpret_cast<f32x4_a4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) p[i] = v[i];
+    }
+  }
+};
+
+// Where a lane works: expert, first row and column, and how many of its columns there are.
+struct Place {
+  int64_t e;
+  int h, c, n;
+};
+__device__ __forceinline__ Place place(int H, int N) {
+  const int across = (N + 64 * kCols4 - 1) / (64 * kCols4), down = (H + kWaves4 * kRows4 - 1) / (kWaves4 * kRows4);
+  const uint32_t b = blockIdx.x, r = b / across;
+  Place p;
+  p.c = (int)(b % across) * 64 * kCols4 + (threadIdx.x & 63) * kCols4;
+  p.h = (int)(r % down) * kWaves4 * kRows4 + (threadIdx.x >> 6) * kRows4;
+  p.e = r / down;
+  p.n = N - p.c;
+  return p;
+}
+
+// w / s for the reciprocal y = 1 / s, exactly rounded (a quotient, its exact rest and one more step: Markstein's
+// theorem), as the code of the nearest whole number within [-8, 7] in the low four bits, 8 added.
+__device__ __forceinline__ uint32_t code_of(float w, float s, float y) {
+  float q = w * y;
+  q = __builtin_fmaf(__builtin_fmaf(-q, s, w), y, q);
+  q = __builtin_amdgcn_fmed3f(q, -8.f, 7.f);
+  return __float_as_uint(q + 12582920.f) & 15u;  // 1.5 * 2^23 + 8: the sum's last bit is worth 1
+}
+
+template <typename T, int G>
+__global__ __launch_bounds__(kWaves4 * 64) void save4_tiles(const T* __restrict__ W, int32_t* __restrict__ codes,
+                                                            uint16_t* __restrict__ scales, int H, int N) {
+  constexpr int kShare = G / kRows4;  // waves of a group
+  __shared__ u32x4 largest[kWaves4][64];
+  const Place at = place(H, N);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int rows = min(kRows4, H - at.h);  // 0 or less: only here for the barrier
+  Four<T> w[kRows4];
+  uint32_t top[4] = {0u, 0u, 0u, 0u};
+  const T* p = W + (at.e * H + at.h) * N + at.c;
+#pragma unroll
+  for (int r = 0; r < kRows4; ++r) w[r].load(p + (int64_t)r * N, r < rows ? at.n : 0);
+#pragma unroll
+  for (int r = 0; r < kRows4; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = w[r].bits(i) & 0x7fffffffu;
+      top[i] = m > top[i] ? m : top[i];
+    }
+  if constexpr (kShare > 1) {
+    largest[wave][lane] = u32x4{top[0], top[1], top[2], top[3]};
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kShare; ++k) {
+      const u32x4 m = largest[wave / kShare * kShare + k][lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i] = m[i] > top[i] ? m[i] : top[i];
+    }
+  }
+  if (rows <= 0 || at.n <= 0) return;
+  float s[4], y[4];
+  uint16_t s16[4];
+  bool plain = true;  // the reciprocals are far from float32's ends
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s16[i] = top[i] < 0x7f800000u ? f32_to_bf16(__uint_as_float(top[i]) / 7.f) : 0x7fc0;
+    s[i] = bf16_to_f32(s16[i]);
+    y[i] = 1.f / s[i];
+    plain &= (s[i] > 0x1p-100f) & (s[i] < 0x1p100f);
+  }
+  const int groups = (H + G - 1) / G, J = (H + 7) / 8;
+  uint16_t* sp = scales + (at.e * groups + at.h / G) * N + at.c;
+  if (at.h % G == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < at.n) sp[i] = s16[i];
+  }
+  int32_t* out = codes + (at.e * J + at.h / 8) * N + at.c;
+#pragma unroll
+  for (int j = 0; j < kRows4 / 8; ++j) {
+    if (8 * j >= rows) break;
+    u32x4 word = (u32x4)(0u);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = __uint_as_float(w[8 * j + r].bits(i));
+        uint32_t code;
+        if (plain) code = code_of(v, s[i], y[i]);
+        else code = s[i] > 0.f ? (uint32_t)((int)fminf(fmaxf(rintf(v / s[i]), -8.f), 7.f) + 8) : 8u;
+        word[i] |= code << code4_bit(r);
+      }
+    int32_t* o = out + (int64_t)j * N;
+    if (at.n >= 4) {
+      *reinterpret_cast<u32x4_a4*>(o) = word;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < at.n) o[i] = (int32_t)word[i];
+    }
   }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void load4_columns(const int32_t* __restrict__ codes,
-                                                     const uint16_t* __restrict__ scales, T* __restrict__ W, int H,
-                                                     int N, int G) {
-  const int groups = (H + G - 1) / G, J = (H + 7) / 8;
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  const int64_t e = blockIdx.y / groups;
-  const int g = blockIdx.y % groups;
-  if (c >= N) return;
-  const float s = bf16_to_f32(scales[(e * groups + g) * N + c]);
-  const int h1 = min(H, (g + 1) * G);
-  for (int h = g * G; h < h1; ++h) {
-    const float v = (float)code4((uint32_t)codes[(e * J + h / 8) * N + c], h % 8) * s;
-    if constexpr (sizeof(T) == 2) W[(e * H + h) * N + c] = f32_to_bf16(v);
-    else W[(e * H + h) * N + c] = v;
+__global__ __launch_bounds__(kWaves4 * 64) void load4_tiles(const int32_t* __restrict__ codes,
+                                                            const uint16_t* __restrict__ scales, T* __restrict__ W,
+                                                            int H, int N, int G) {
+  const Place at = place(H, N);
+  const int rows = min(kRows4, H - at.h), groups = (H + G - 1) / G, J = (H + 7) / 8;
+  if (rows <= 0 || at.n <= 0) return;
+  const int32_t* in = codes + (at.e * J + at.h / 8) * N + at.c;
+  u32x4 word[kRows4 / 8];
+#pragma unroll
+  for (int j = 0; j < kRows4 / 8; ++j) {
+    const int32_t* q = in + (int64_t)(8 * j < rows ? j : 0) * N;
+    if (at.n >= 4) {
+      word[j] = *reinterpret_cast<const u32x4_a4*>(q);
+    } else {
+      word[j] = (u32x4)(0u);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < at.n) word[j][i] = (uint32_t)q[i];
+    }
+  }
+  Four<uint16_t> s;
+  s.load(scales + (at.e * groups + at.h / G) * N + at.c, at.n);
+  T* out = W + (at.e * H + at.h) * N + at.c;
+#pragma unroll
+  for (int r = 0; r < kRows4; ++r) {
+    if (r >= rows) break;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)code4(word[r / 8][i], r % 8) * __uint_as_float(s.bits(i));
+    Four<T>::store(out + (int64_t)r * N, v, at.n);
   }
 }
 
@@ -72,7 +211,22 @@ int check4(const char* who, int32_t E, int32_t H, int32_t N, int32_t G, moonep_d
   MOONEP_REQUIRE(N >= 1 && N <= kMaxWidth, "%s: N must be in [1, %d] (got %d)", who, kMaxWidth, N);
   MOONEP_REQUIRE(G == 32 || G == 64 || G == 128, "%s: G must be 32, 64 or 128 (got %d)", who, G);
   MOONEP_REQUIRE(t == MOONEP_F32 || t == MOONEP_BF16, "%s: bad dtype %d", who, (int)t);
+  MOONEP_REQUIRE((int64_t)E * ceil_div_u(H, kWaves4 * kRows4) * ceil_div_u(N, 64 * kCols4) < (int64_t(1) << 31),
+                 "%s: grid too large", who);
   return MOONEP_OK;
+}
+
+dim3 tiles4(int32_t E, int32_t H, int32_t N) {
+  return dim3((unsigned)((int64_t)E * ceil_div_u(H, kWaves4 * kRows4) * ceil_div_u(N, 64 * kCols4)));
+}
+
+template <typename T>
+void save4(dim3 grid, hipStream_t s, const void* W, int32_t* codes, uint16_t* scales, int H, int N, int G) {
+  const T* w = static_cast<const T*>(W);
+  const dim3 block(kWaves4 * 64);
+  if (G == 32) hipLaunchKernelGGL((save4_tiles<T, 32>), grid, block, 0, s, w, codes, scales, H, N);
+  else if (G == 64) hipLaunchKernelGGL((save4_tiles<T, 64>), grid, block, 0, s, w, codes, scales, H, N);
+  else hipLaunchKernelGGL((save4_tiles<T, 128>), grid, block, 0, s, w, codes, scales, H, N);
 }
 
 }  // namespace
@@ -88,13 +242,9 @@ extern "C" int moonep_save4(int32_t E, int32_t H, int32_t N, int32_t G, moonep_d
   MOONEP_REQUIRE(aligned(W, elem_bytes(t)) && aligned(codes, 4) && aligned(scales, 2),
                  "moonep_save4: a pointer is not aligned to its elements");
   clear_stale_error();
-  const dim3 grid(ceil_div_u(N, 256), (unsigned)(E * ((H + G - 1) / G)));
-  if (t == MOONEP_BF16)
-    hipLaunchKernelGGL(save4_columns<uint16_t>, grid, dim3(256), 0, as_stream(stream), (const uint16_t*)W, codes,
-                       scales, H, N, G);
-  else
-    hipLaunchKernelGGL(save4_columns<float>, grid, dim3(256), 0, as_stream(stream), (const float*)W, codes, scales, H,
-                       N, G);
+  const dim3 grid = tiles4(E, H, N);
+  if (t == MOONEP_BF16) save4<uint16_t>(grid, as_stream(stream), W, codes, scales, H, N, G);
+  else save4<float>(grid, as_stream(stream), W, codes, scales, H, N, G);
   MOONEP_LAUNCH_CHECK("moonep_save4");
   return MOONEP_OK;
 }
@@ -107,12 +257,11 @@ extern "C" int moonep_load4(int32_t E, int32_t H, int32_t N, int32_t G, moonep_d
   MOONEP_REQUIRE(aligned(W, elem_bytes(t)) && aligned(codes, 4) && aligned(scales, 2),
                  "moonep_load4: a pointer is not aligned to its elements");
   clear_stale_error();
-  const dim3 grid(ceil_div_u(N, 256), (unsigned)(E * ((H + G - 1) / G)));
+  const dim3 grid = tiles4(E, H, N), block(kWaves4 * 64);
   if (t == MOONEP_BF16)
-    hipLaunchKernelGGL(load4_columns<uint16_t>, grid, dim3(256), 0, as_stream(stream), codes, scales, (uint16_t*)W, H,
-                       N, G);
+    hipLaunchKernelGGL(load4_tiles<uint16_t>, grid, block, 0, as_stream(stream), codes, scales, (uint16_t*)W, H, N, G);
   else
-    hipLaunchKernelGGL(load4_columns<float>, grid, dim3(256), 0, as_stream(stream), codes, scales, (float*)W, H, N, G);
+    hipLaunchKernelGGL(load4_tiles<float>, grid, block, 0, as_stream(stream), codes, scales, (float*)W, H, N, G);
   MOONEP_LAUNCH_CHECK("moonep_load4");
   return MOONEP_OK;
 }
