@@ -528,7 +528,8 @@ int moonep_few_ffn(moonep_dims d, int32_t H, int32_t Hp, moonep_dtype t, const v
  */
 
 /*
- * moonep_save4 -- weights into 4 bits: scale = (largest magnitude of the group) / 7, rounded to bfloat16;
+ * moonep_save4 -- weights into 4 bits: scale = (largest magnitude of the group) * (1/7), a float32 product rounded to
+ *   bfloat16;
  *   code = value / scale rounded to the nearest even whole number, held within [-8, 7] (0 where the scale is 0).
  *   A group with an infinity or a NaN has the scale NaN.
  * moonep_load4 -- the values that 4-bit weights stand for (float32: exactly; bf16: rounded once).

@@ -1,6 +1,6 @@
 // moonep_save4 / moonep_load4: an expert weight tensor [E, H, N] into 4 bits with a scale per column and G rows, and back.
 //
-// scale = bf16(max |w| / 7), code = w / scale rounded to even within [-8, 7]; both quotients are exactly rounded, so
+// scale = bf16(max |w| * (1/7)), code = w / scale rounded to even within [-8, 7], the quotient exactly rounded, so that
 // the codes are those of the formula in float32.  A group that holds an infinity or a NaN has the scale NaN.
 //
 // Both are HBM streams.  A lane takes four columns of 32 rows (whole 512-byte to 1 KB pieces of a row to a wave), a block
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kWaves4 * 64) void save4_tiles(const T* __restrict_
   bool plain = true;  // the reciprocals are far from float32's ends
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    s16[i] = top[i] < 0x7f800000u ? f32_to_bf16(__uint_as_float(top[i]) / 7.f) : 0x7fc0;
+    s16[i] = top[i] < 0x7f800000u ? f32_to_bf16(__uint_as_float(top[i]) * (1.f / 7.f)) : 0x7fc0;
     s[i] = bf16_to_f32(s16[i]);
     y[i] = 1.f / s[i];
     plain &= (s[i] > 0x1p-100f) & (s[i] < 0x1p100f);

@@ -7,7 +7,7 @@ Router scores of a token's logits l: softmax(l) or sigmoid(l); NaN and -inf mask
 counts as the largest float32.  The K experts are the largest l, or with a bias the largest score + bias, descending, the
 lowest id first among equals; -1 (gate 0) where fewer are left.
 
-4-bit weights: per column and G rows, scale = bfloat16(float32(largest magnitude / 7)), code = the nearest whole number
+4-bit weights: per column and G rows, scale = bfloat16(float32(largest magnitude * float32(1/7))), code = the nearest whole number
 (ties to even) to the float32 quotient of value and scale, held within [-8, 7].
 """
 from __future__ import annotations
@@ -137,7 +137,7 @@ def save4(W, G: int):
         w = W[:, g * G:(g + 1) * G]
         ok = np.isfinite(w).all(axis=1)
         top = np.where(ok, np.abs(np.where(np.isfinite(w), w, 0)).max(axis=1), 0).astype(np.float32)
-        s = _bf16(top / np.float32(7))
+        s = _bf16(top * np.float32(1 / 7))
         with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
             q = np.clip(np.rint(np.where(np.isfinite(w), w, 0) / s[:, None]), -8, 7)
         codes[:, g * G:(g + 1) * G] = np.where((ok & (s > 0))[:, None], q, 0)
