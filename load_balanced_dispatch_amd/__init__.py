@@ -35,5 +35,6 @@ from ._lib import (  # noqa: F401
     moonep_few_workspace_bytes, moonep_few_layer, moonep_few_ffn, moonep_few_layer4, moonep_few_ffn4, moonep_save4,
     moonep_load4,
 )
+from .layer import MoeFew  # noqa: F401
 from .layer import MoeFFN  # noqa: F401
 from .layer import MoeLayer  # noqa: F401

@@ -8,7 +8,8 @@ the plan); the weight backward is
 wgrad -> reduce_grad; with data_grad=True the data backward is
 combine_backward (writes dY and dgates from dout) -> dgrad -> dispatch_backward
 (dX).  Each step is one C-ABI call whose kernels do all the work; this class
-only owns memory and passes pointers.
+only owns memory and passes pointers.  MoeFFN is the same for experts that are
+gated FFNs, and MoeFew that layer for few tokens, without a plan.
 """
 from __future__ import annotations
 
@@ -168,10 +169,15 @@ class MoeFFN:
     output-gradient rows -> dgrad of the down projection -> swiglu backward from 8 bits (which also gives the gated
     activation and dgates) -> wgrad of the down projection -> dispatch from 8 bits -> dgrad and wgrad of the
     gate|up projection -> dispatch backward -> reduce_grad.
+
+    `router="softmax"` or `"sigmoid"` puts the router's choice in front: forward() makes topk_idx and gates from the
+    scores `logits` [R, S, E] (float32, which the caller's router projection writes) and, with router_bias=True, from
+    `bias` [E], which corrects the choice only; `renorm` and `route_scale` are moonep_route's renorm and scale.
+    backward() ends with `dlogits` from dgates.
     """
 
     def __init__(self, R, E, B, S, K, H, Hp, dtype=torch.bfloat16, device="cuda", backward=False, norm=False,
-                 eps=1e-5, save8=False, scratch=None):
+                 eps=1e-5, save8=False, scratch=None, router=None, renorm=True, route_scale=1.0, router_bias=False):
         if save8 and not backward:
             raise ValueError("save8 keeps activations for the backward pass: it needs backward=True")
         if scratch is not None and backward and not save8:
@@ -186,6 +192,9 @@ class MoeFFN:
         N = d.N
         self.topk_idx = torch.zeros((R, S, K), **i32)
         self.gates = torch.zeros((R, S, K), **f32)
+        _router_buffers(self, router, renorm, route_scale, router_bias, f32)
+        if router is not None and backward:
+            self.dlogits = torch.empty((R, S, E), **f32)
         self.expert_counts = torch.zeros(E, **i32)
         self.maxvio = torch.zeros(1, dtype=torch.float64, device=device)
         self.cu_seqlens = torch.zeros((R, E + B + 1), **i32)
@@ -263,7 +272,7 @@ class MoeFFN:
     def forward_calls(self):
         d, H, Hp, L = self.d, self.H, self.Hp, _lib
         sl = self._slots
-        calls = [
+        calls = _route_calls(self) + [
             ("plan", lambda: L.moonep_plan(d, self.topk_idx, self.expert_counts, self.maxvio, self.cu_seqlens,
                                            sl(self.slot_expert), self.dest_idx, self.src_of_row, self.stats,
                                            self.ws_plan)),
@@ -345,6 +354,9 @@ class MoeFFN:
             calls.append(("layernorm_backward", lambda: L.moonep_layernorm_backward(
                 d, H, self.dXn, self.X, self.mean, self.rstd, self.gamma, self.dX, self.dgamma, self.dbeta,
                 self.ws_norm)))
+        if self.router is not None:
+            calls.append(("route_backward", lambda: L.moonep_route_backward(
+                d, self.router, self.renorm, self.route_scale, self.logits, self.topk_idx, self.dgates, self.dlogits)))
         return calls
 
     def forward(self):
@@ -358,3 +370,108 @@ class MoeFFN:
         with torch.cuda.device(self.X.get_device()):
             for _, f in calls:
                 f()
+
+
+def _router_buffers(layer, router, renorm, route_scale, router_bias, f32):
+    """The router's options and buffers of a layer, whose topk_idx and gates forward() then writes."""
+    d = layer.d
+    if router is not None and router not in _lib.SCORES:
+        raise ValueError(f"unknown router score {router!r}; one of {sorted(_lib.SCORES)}")
+    if router_bias and router is None:
+        raise ValueError("router_bias corrects the choice of a router")
+    layer.router, layer.renorm, layer.route_scale = router, renorm, route_scale
+    layer.logits = torch.zeros((d.R, d.S, d.E), **f32) if router is not None else None
+    layer.bias = torch.zeros(d.E, **f32) if router_bias else None
+
+
+def _route_calls(layer):
+    if layer.router is None:
+        return []
+    return [("route", lambda: _lib.moonep_route(layer.d, layer.router, layer.renorm, layer.route_scale, layer.logits,
+                                                layer.bias, layer.topk_idx, layer.gates))]
+
+
+class MoeFew:
+    """Static buffers for one gated expert layer that serves few tokens (R*S*K <= MOONEP_FEW_PAIRS), and its calls.
+
+    forward() writes out [R, S, H] (float32) from X [R, S, H], topk_idx and gates, without a plan: each chosen expert's
+    weights are read once.  `router`, `renorm`, `route_scale`, `router_bias`: as in MoeFFN, topk_idx and gates are then
+    made from `logits`.  `norm=True` puts the layer norm of MoeFFN in front (gamma, beta, eps; its rows, rounded to
+    dtype, are in Xn).
+
+    The weights are the home weights of MoeFFN, W_gu [E, H, 2H'] and W_down [E, H', H] of `dtype`, or with bits=4 their
+    4-bit form with groups of G input rows: gu_codes, gu_scales, down_codes, down_scales, which save_weights() writes.
+    `weights` = those tensors in that order makes the layer use a caller's, such as a MoeFFN's W_gu_home and
+    W_down_home or another MoeFew's.
+    """
+
+    def __init__(self, R, E, S, K, H, Hp, dtype=torch.bfloat16, device="cuda", norm=False, eps=1e-5, bits=16, G=32,
+                 weights=None, router=None, renorm=True, route_scale=1.0, router_bias=False):
+        if bits not in (4, 16):
+            raise ValueError(f"bits must be 16 (weights of dtype) or 4 (got {bits})")
+        if bits == 4 and G not in (32, 64, 128):
+            raise ValueError(f"G must be 32, 64 or 128 (got {G})")
+        self.d: Dims = make_dims(R, E, 0, S, K)
+        d = self.d
+        if d.N > _lib.MOONEP_FEW_PAIRS:
+            raise ValueError(f"R*S*K ({d.N}) exceeds {_lib.MOONEP_FEW_PAIRS}: MoeFFN is for as many tokens")
+        self.H, self.Hp, self.dtype, self.device = H, Hp, dtype, device
+        self.norm, self.eps, self.bits, self.G = norm, eps, bits, G
+        f32 = dict(dtype=torch.float32, device=device)
+        self.topk_idx = torch.zeros((R, S, K), dtype=torch.int32, device=device)
+        self.gates = torch.zeros((R, S, K), **f32)
+        _router_buffers(self, router, renorm, route_scale, router_bias, f32)
+        self.X = torch.zeros((R, S, H), dtype=dtype, device=device)
+        if norm:
+            self.gamma = torch.ones(H, **f32)
+            self.beta = torch.zeros(H, **f32)
+            self.Xn = torch.empty((R, S, H), dtype=dtype, device=device)
+        self.out = torch.empty((R, S, H), **f32)
+        self.workspace = torch.empty(max(1, _lib.moonep_few_workspace_bytes(d, H, Hp)), dtype=torch.uint8, device=device)
+        if bits == 4:
+            i32, bf16 = dict(dtype=torch.int32, device=device), dict(dtype=torch.bfloat16, device=device)
+            form = []
+            for rows, cols in ((H, 2 * Hp), (Hp, H)):
+                form += [((E, -(-rows // 8), cols), i32), ((E, -(-rows // G), cols), bf16)]
+            names = ("gu_codes", "gu_scales", "down_codes", "down_scales")
+        else:
+            form = [(shape, dict(dtype=dtype, device=device)) for shape in ((E, H, 2 * Hp), (E, Hp, H))]
+            names = ("W_gu", "W_down")
+        if weights is None:
+            weights = [torch.zeros(shape, **kind) for shape, kind in form]
+        if len(weights) != len(form):
+            raise ValueError(f"weights must be {', '.join(names)}")
+        for name, t, (shape, kind) in zip(names, weights, form):
+            if tuple(t.shape) != shape or t.dtype != kind["dtype"] or not t.is_contiguous() or t.device != self.X.device:
+                raise ValueError(f"{name} must be {list(shape)} {kind['dtype']}, contiguous, on {self.X.device}")
+            setattr(self, name, t)
+
+    def save_weights(self, W_gu, W_down):
+        """Writes weights [E, H, 2H'] and [E, H', H] (bfloat16 or float32) as the layer keeps them."""
+        E, H, Hp = self.d.E, self.H, self.Hp
+        if self.bits == 4:
+            _lib.moonep_save4(E, H, 2 * Hp, self.G, W_gu, self.gu_codes, self.gu_scales)
+            _lib.moonep_save4(E, Hp, H, self.G, W_down, self.down_codes, self.down_scales)
+        else:
+            self.W_gu.copy_(W_gu)
+            self.W_down.copy_(W_down)
+
+    def forward_calls(self):
+        d, H, Hp, L = self.d, self.H, self.Hp, _lib
+        calls = _route_calls(self)
+        if self.norm:
+            calls.append(("layernorm", lambda: L.moonep_layernorm(d, H, self.X, self.gamma, self.beta, self.eps, self.Xn,
+                                                                  None, None)))
+        rows = (self.Xn if self.norm else self.X, self.topk_idx, self.gates)
+        if self.bits == 4:
+            calls.append(("few_ffn4", lambda: L.moonep_few_ffn4(d, H, Hp, self.G, *rows, self.gu_codes, self.gu_scales,
+                                                                self.down_codes, self.down_scales, self.out,
+                                                                self.workspace)))
+        else:
+            calls.append(("few_ffn", lambda: L.moonep_few_ffn(d, H, Hp, *rows, self.W_gu, self.W_down, self.out,
+                                                              self.workspace)))
+        return calls
+
+    def forward(self):
+        for _, f in self.forward_calls():
+            f()
