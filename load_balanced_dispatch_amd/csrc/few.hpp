@@ -39,13 +39,15 @@ typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 __device__ __forceinline__ bf16x8 as_operand(u32x4 q) { return __builtin_bit_cast(bf16x8, q); }
 
-// A row source gives lane l the values of columns k .. k + 7 of a row of activations: kPer rows of the instruction make up
-// one of them, and the last kPer - 1 are added with the waves' sums.  A float32 row is three rows of bf16, 8 bits of
-// each value's 24 at a time, cut off and not rounded, so that no part overflows.
+// A row source gives lane l the values of columns k .. k + 7 of a row of activations, as S operands whose products are
+// added into one sum.  A float32 row is three parts in bf16, 8 bits of each value's 24 at a time, cut off and not
+// rounded, so that no part overflows.  The parts are kPer = 3 rows of one instruction (a third of the loads and
+// instructions of three operands), added with the waves' sums.  Wide is the source for more pairs than that holds.
 
 // Rows of bf16 or float32 values, columns from H on 0.
 struct RowsBf16 {
-  static constexpr int kPer = 1;
+  static constexpr int kPer = 1, S = 1;
+  typedef RowsBf16 Wide;
   const uint16_t* x;
   int H;
   typedef u32x4 Raw;
@@ -59,10 +61,12 @@ struct RowsBf16 {
       if (k + i < H) q[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
     return q;
   }
-  static __device__ __forceinline__ bf16x8 operand(const Raw& q) { return as_operand(q); }
+  static __device__ __forceinline__ void operands(const Raw& q, bf16x8 (&a)[1]) { a[0] = as_operand(q); }
+  __device__ __forceinline__ const Wide& wide() const { return *this; }
 };
 struct RowsF32 {  // for the float32 instruction
-  static constexpr int kPer = 1;
+  static constexpr int kPer = 1, S = 1;
+  typedef RowsF32 Wide;
   const float* x;
   int H;
   struct Raw {
@@ -85,28 +89,53 @@ struct RowsF32 {  // for the float32 instruction
     }
     return r;
   }
+  __device__ __forceinline__ const Wide& wide() const { return *this; }
 };
-struct RowsSplit {  // float32 rows as parts, for 4-bit weights
-  static constexpr int kPer = 3;
+// float32 rows as parts, for 4-bit weights.  An infinity's rest is no number, and so is its product.
+struct RowsSplitWide {
+  static constexpr int kPer = 1, S = 3;
+  RowsF32 rows;
+  typedef RowsF32::Raw Raw;
+  template <bool TAIL>
+  __device__ __forceinline__ Raw load(int64_t row, int k) const { return rows.load<TAIL>(row, k); }
+  static __device__ __forceinline__ float rest(float v) { return v - __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+  static __device__ __forceinline__ bf16x8 tops(const float (&f)[8]) {
+    u32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = __builtin_amdgcn_perm(__float_as_uint(f[2 * i + 1]), __float_as_uint(f[2 * i]), 0x07060302u);
+    return as_operand(q);
+  }
+  static __device__ __forceinline__ void operands(const Raw& r, bf16x8 (&a)[3]) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = r.f[i];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      a[s] = tops(f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = rest(f[i]);
+    }
+  }
+};
+struct RowsSplit {
+  static constexpr int kPer = 3, S = 1;
+  typedef RowsSplitWide Wide;
   RowsF32 rows;
   typedef RowsF32::Raw Raw;
   template <bool TAIL>
   __device__ __forceinline__ Raw load(int64_t row, int k) const { return rows.load<TAIL>(row / 3, k); }
-  static __device__ __forceinline__ bf16x8 operand(const Raw& r) {
+  static __device__ __forceinline__ void operands(const Raw& r, bf16x8 (&a)[1]) {
     const int part = (threadIdx.x & 15) % 3;  // of the lane's row
-    uint32_t h[8];
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t top = __float_as_uint(r.f[i]);
-      const float rest = r.f[i] - __uint_as_float(top & 0xffff0000u);  // an infinity's is no number, nor is its product
-      const float low = rest - __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-      h[i] = part == 0 ? top : __float_as_uint(part == 1 ? rest : low);
+      const float mid = Wide::rest(r.f[i]), low = Wide::rest(mid);
+      f[i] = part == 0 ? r.f[i] : part == 1 ? mid : low;
     }
-    u32x4 q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_perm(h[2 * i + 1], h[2 * i], 0x07060302u);
-    return as_operand(q);
+    a[0] = Wide::tops(f);
   }
+  __device__ __forceinline__ Wide wide() const { return {rows}; }
 };
 
 // silu(g) * u, with exp of non-positive arguments only
@@ -116,17 +145,19 @@ __device__ __forceinline__ float gated(float g, float u) {
   return g * (g >= 0.f ? r : e * r) * u;
 }
 
-// The activation between the two products as few_mfma writes it: [pairs, 3, wide] bf16 parts, padded with zeros.
+// The activation between the two products as few_mfma writes it: [pairs, 3, columns] bf16 parts, padded with zeros.
 struct RowsParts {
-  static constexpr int kPer = 3;
+  static constexpr int kPer = 3, S = 1;
+  typedef RowsParts Wide;
   const uint16_t* x;
-  int wide;
+  int columns;
   typedef u32x4 Raw;
   template <bool TAIL>
   __device__ __forceinline__ Raw load(int64_t row, int k) const {
-    return *reinterpret_cast<const u32x4*>(x + row * wide + k);
+    return *reinterpret_cast<const u32x4*>(x + row * columns + k);
   }
-  static __device__ __forceinline__ bf16x8 operand(const Raw& q) { return as_operand(q); }
+  static __device__ __forceinline__ void operands(const Raw& q, bf16x8 (&a)[1]) { a[0] = as_operand(q); }
+  __device__ __forceinline__ const Wide& wide() const { return *this; }
 };
 
 // ------------------------------------------------------------------ weights
@@ -176,9 +207,9 @@ struct WeightsBf16 {
   }
   template <int MT, class R>
   static __device__ __forceinline__ void mac(f32x4 (&acc)[MT][V], const Raw& r, const typename R::Raw (&x)[MT]) {
-    bf16x8 a[MT];
+    bf16x8 a[MT][R::S];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) a[t] = R::operand(x[t]);
+    for (int t = 0; t < MT; ++t) R::operands(x[t], a[t]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       u32x4 q;
@@ -187,7 +218,9 @@ struct WeightsBf16 {
         q[p] = __builtin_amdgcn_perm(r.d[2 * p + 1][j / 2], r.d[2 * p][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
       const bf16x8 b = as_operand(q);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t][j] = mfma16(a[t], b, acc[t][j]);
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int s = 0; s < R::S; ++s) acc[t][j] = mfma16(a[t][s], b, acc[t][j]);
     }
   }
 };
@@ -274,13 +307,15 @@ struct WeightsFour {
   }
   template <int MT, class R>
   static __device__ __forceinline__ void mac(f32x4 (&acc)[MT][V], const Raw& r, const typename R::Raw (&x)[MT]) {
-    bf16x8 a[MT];
+    bf16x8 a[MT][R::S];
     f32x4 start[MT];
     const bf16x8 less = as_operand((u32x4)(0xc1c0c1c0u));  // -24
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      a[t] = R::operand(x[t]);
-      start[t] = mfma16(a[t], less, f32x4{0.f, 0.f, 0.f, 0.f});
+      R::operands(x[t], a[t]);
+      start[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < R::S; ++s) start[t] = mfma16(a[t][s], less, start[t]);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -291,7 +326,9 @@ struct WeightsFour {
       const float scale = __uint_as_float(j % 2 ? r.s[j / 2] & 0xffff0000u : r.s[j / 2] << 16);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const f32x4 part = mfma16(a[t], b, start[t]);
+        f32x4 part = start[t];
+#pragma unroll
+        for (int s = 0; s < R::S; ++s) part = mfma16(a[t][s], b, part);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][j][i] = __builtin_fmaf(scale, part[i], acc[t][j][i]);
       }
@@ -366,17 +403,32 @@ __device__ __forceinline__ void few_steps(const W& w, const R& rows, const typen
 #pragma unroll
       for (int g = 0; g < NG; ++g) W::template mac<MT, R>(acc[g], r[u][g], x[u]);
   }
-  for (; s < steps; s += stride) {
-    const int k = s * kStep + kl;
-    typename W::Raw r[NG];
-    typename R::Raw x[MT];
+  // what is left, at most U steps: together too
+  if (s >= steps) return;
+  typename W::Raw r[U][NG];
+  typename R::Raw x[U][MT];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) r[g] = w.template load<true>(at[g], k);
+  for (int u = 0; u < U; ++u) {
+    const int k = (s + u * stride) * kStep + kl;
+    if (s + u * stride < full) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) x[t] = rows.template load<true>(row[t], k);
+      for (int g = 0; g < NG; ++g) r[u][g] = w.template load<false>(at[g], k);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) W::template mac<MT, R>(acc[g], r[g], x);
+      for (int t = 0; t < MT; ++t) x[u][t] = rows.template load<false>(row[t], k);
+    } else if (s + u * stride < steps) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) r[u][g] = w.template load<true>(at[g], k);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) x[u][t] = rows.template load<true>(row[t], k);
+    }
   }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (s + u * stride < steps) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) W::template mac<MT, R>(acc[g], r[u][g], x[u]);
+    }
 }
 
 // The products of up to MT matrix instructions' rows, `here` of the block's pairs, for a tile of 16 * V columns of KW
@@ -453,9 +505,14 @@ __device__ __forceinline__ void few_tile(const W& w, const R& rows, const O& out
   __syncthreads();
 }
 
+// Three operands a row would take a few registers more than let four waves share a SIMD: held to those, with a few
+// addresses spilled, 12 float32 rows through 16 experts of 1413 x 1531 in 4 bits 14.2 us (15.4 without; all pairs as packed
+// rows 17.0).
 template <class W, class R, class O, int MT, int NW, int KW>
-__global__ __launch_bounds__(NW * 64) void few_mfma(W w, R rows, O out, Pairs pairs, int H, int C) {
-  constexpr int TW = 16 * W::kV, PT = kRows / R::kPer, U = O::kGated ? W::kGatedU : W::kPlainU;
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(R::Wide::S > 1 ? 4 : 2))) void few_mfma(W w, R rows, O out, Pairs pairs, int H, int C) {
+  typedef typename R::Wide Wide;
+  constexpr int TW = 16 * W::kV, PT = kRows / Wide::kPer;
+  constexpr int U = O::kGated ? W::kGatedU : W::kPlainU, kWideU = U > 1 && Wide::S > 1 ? U / 2 : U;
   extern __shared__ float lds[];  // sums [NW][kRows][TW], then the block's pairs
   int32_t* list = reinterpret_cast<int32_t*>(lds + NW * kRows * TW);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -481,8 +538,12 @@ __global__ __launch_bounds__(NW * 64) void few_mfma(W w, R rows, O out, Pairs pa
   __syncthreads();
   for (int m0 = 0; m0 < m; m0 += MT * PT) {
     const int here = min(m - m0, MT * PT);
-    if (MT > 1 && here <= PT) few_tile<W, R, O, 1, NW, KW, U>(w, rows, out, pairs.per, H, C, e, lds, list + m0, here, tile);
-    else few_tile<W, R, O, MT, NW, KW, MT == 1 ? U : 1>(w, rows, out, pairs.per, H, C, e, lds, list + m0, here, tile);
+    if (R::kPer > Wide::kPer && here <= kRows / R::kPer)
+      few_tile<W, R, O, 1, NW, KW, U>(w, rows, out, pairs.per, H, C, e, lds, list + m0, here, tile);
+    else if (MT == 1 || here <= PT)
+      few_tile<W, Wide, O, 1, NW, KW, kWideU>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
+    else
+      few_tile<W, Wide, O, MT, NW, KW, 1>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
   }
 }
 
@@ -586,9 +647,8 @@ void launch(const Call& c, const Product& p, W w, R rows, O out) {
 
 template <class W, class R, class O>
 void by_expert(const Call& c, const Product& p, W w, R rows, O out) {
-  constexpr int PT = kRows / R::kPer;
   if constexpr (W::kV == 1) {
-    launch<W, R, O, 2, kWaves, 8>(c, p, w, rows, out);
+    launch<W, R, O, 1, kWaves, 8>(c, p, w, rows, out);
   } else {
     const int64_t tiles = (int64_t)c.rows() * ceil_div_u(p.width, 16 * W::kV);
     // Waves one after the other along the input rows: enough of them for the chip, and more while each keeps 20 steps
@@ -603,11 +663,12 @@ void by_expert(const Call& c, const Product& p, W w, R rows, O out) {
       else if (kw == 4) launch<W, R, O, MT, kWaves, 4>(c, p, w, rows, out);
       else launch<W, R, O, MT, kWaves, 2>(c, p, w, rows, out);
     };
-    // Two instructions' rows side by side where a token more than one holds could choose the same expert: twice the sums in
-    // registers, but its weights read once (32 tokens, 256 experts: 1811 against 1835 us; four side by side won 6% with bf16
-    // and lost 6% with 4-bit weights at 128 tokens and 64 experts).
-    if (c.T() <= PT) with(std::integral_constant<int, 1>{});
-    else with(std::integral_constant<int, 2>{});
+    // Two instructions' rows side by side where more tokens than one holds could choose the same expert: twice the sums in
+    // registers, but its weights read once (32 tokens, 256 experts: 1811 against 1835 us).  Three operands need no more.
+    constexpr int PT = kRows / R::Wide::kPer;
+    if constexpr (R::Wide::S == 1)
+      if (c.T() > PT) return with(std::integral_constant<int, 2>{});
+    with(std::integral_constant<int, 1>{});
   }
 }
 
