@@ -464,7 +464,7 @@ typedef enum moonep_score {
  *   other calls leave out) and gate 0 in the places that are left.
  * In:  logits [R,S,E] float32;  bias [E] float32 or NULL.
  * Out: topk_idx [R,S,K] int32;  gates [R,S,K] float32.
- * E <= 4096; B is not used.
+ * E <= 4096, R*S <= 2^25; B is not used.
  */
 int moonep_route(moonep_dims d, int32_t score, int32_t renorm, float scale, const float* logits, const float* bias,
                  int32_t* topk_idx, float* gates, moonep_stream stream);
@@ -490,7 +490,8 @@ int moonep_route_backward(moonep_dims d, int32_t score, int32_t renorm, float sc
  * read each chosen expert's home weights once and need no plan.  They take R*S*K <= MOONEP_FEW_PAIRS pairs
  * (MOONEP_EINVAL beyond: the planned calls are for those), H and Hp up to 65536, and use of d only R, E, S and K.
  * Products and sums are float32 and nothing is rounded to dtype t on the way.  Pairs whose id is outside [0, E) are
- * left out.  Results are the same from call to call.
+ * left out; an expert that a token holds twice counts twice.  Results are the same from call to call.  Pointers need the
+ * alignment of their elements only.
  */
 enum { MOONEP_FEW_PAIRS = 1024 };
 

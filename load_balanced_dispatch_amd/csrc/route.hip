@@ -15,6 +15,7 @@ namespace moonep {
 namespace {
 
 constexpr int kMaxE = 4096;
+constexpr int kMaxTokens = 1 << 25;  // 64 lanes each: a grid of fewer than 2^32
 constexpr float kLargest = 3.402823466e38f;
 constexpr int kNone = 0x7fffffff;  // no expert: after every index
 constexpr int kRowE = 512, kRowK = 15;  // most experts and choices of a token in 16 lanes
@@ -574,7 +575,7 @@ void by_size(const Route& r, F f) {
 int check_route(const char* who, const moonep_dims& d, int32_t score, float scale) {
   if (int rc = check_dims(d, who)) return rc;
   MOONEP_REQUIRE(d.E <= kMaxE, "%s: E (%d) exceeds %d", who, d.E, kMaxE);
-  MOONEP_REQUIRE((int64_t)d.R * d.S < (int64_t(1) << 31), "%s: R*S must be < 2^31", who);
+  MOONEP_REQUIRE((int64_t)d.R * d.S <= kMaxTokens, "%s: R*S (%lld) exceeds %d", who, (long long)d.R * d.S, kMaxTokens);
   MOONEP_REQUIRE(score == MOONEP_SCORE_SOFTMAX || score == MOONEP_SCORE_SIGMOID, "%s: bad score %d", who, score);
   MOONEP_REQUIRE(scale - scale == 0.f, "%s: scale must be finite", who);
   return MOONEP_OK;

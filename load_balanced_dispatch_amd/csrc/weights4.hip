@@ -211,7 +211,7 @@ int check4(const char* who, int32_t E, int32_t H, int32_t N, int32_t G, moonep_d
   MOONEP_REQUIRE(N >= 1 && N <= kMaxWidth, "%s: N must be in [1, %d] (got %d)", who, kMaxWidth, N);
   MOONEP_REQUIRE(G == 32 || G == 64 || G == 128, "%s: G must be 32, 64 or 128 (got %d)", who, G);
   MOONEP_REQUIRE(t == MOONEP_F32 || t == MOONEP_BF16, "%s: bad dtype %d", who, (int)t);
-  MOONEP_REQUIRE((int64_t)E * ceil_div_u(H, kWaves4 * kRows4) * ceil_div_u(N, 64 * kCols4) < (int64_t(1) << 31),
+  MOONEP_REQUIRE((int64_t)E * ceil_div_u(H, kWaves4 * kRows4) * ceil_div_u(N, 64 * kCols4) < (int64_t(1) << 24),
                  "%s: grid too large", who);
   return MOONEP_OK;
 }

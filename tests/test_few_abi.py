@@ -126,6 +126,8 @@ def test_router_arguments():
             assert "scale" in m.last_error()
         assert call(m.make_dims(1, 4097, 0, 3, 2), P[:n]) == _lib.MOONEP_EINVAL
         assert "exceeds 4096" in m.last_error()
+        assert call(m.make_dims(1, 4, 0, (1 << 25) + 1, 2), P[:n]) == _lib.MOONEP_EINVAL
+        assert "exceeds 33554432" in m.last_error()
     with pytest.raises(ValueError, match="unknown score"):
         m.moonep_route(D, "tanh", True, 1.0, None, None, None, None)
 
@@ -135,6 +137,8 @@ def test_sizes_of_4_bit_weights():
         for E, H, N in ((-1, 8, 8), (2, 0, 8), (2, 8, 0), (2, 65537, 8), (2, 8, 65537)):
             assert call(E, H, N, 32, BF, P[:3]) == _lib.MOONEP_EINVAL
             assert "must be" in m.last_error()
+        assert call(1 << 20, 4096, 8192, 32, BF, P[:3]) == _lib.MOONEP_EINVAL
+        assert "grid too large" in m.last_error()
         assert call(2, 8, 8, 32, 9, P[:3]) == _lib.MOONEP_EINVAL
         assert "dtype" in m.last_error()
 

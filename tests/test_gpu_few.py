@@ -219,6 +219,9 @@ DTYPES = [(BF, 16), (F32, 16), (BF, 4), (F32, 4)]
 LAYERS = [(1, 1, 1, 1, 1), (1, 2, 2, 7, 3), (3, 4, 2, 8, 8), (2, 5, 3, 31, 9), (5, 8, 2, 32, 16), (4, 3, 1, 33, 17),
           (1, 16, 8, 64, 64), (16, 4, 2, 65, 65), (17, 3, 2, 100, 127), (8, 16, 4, 128, 128), (3, 6, 2, 253, 130),
           (33, 5, 3, 96, 40), (2, 4, 2, 1413, 259), (64, 8, 2, 72, 136), (1, 4, 2, 2048, 1408)]
+# enough tiles for wide ones and for few waves to each; more than 64 pairs with more experts yet; more than 8 and 16 choices
+LAYERS += [(40, 64, 2, 64, 1030), (40, 48, 2, 70, 1030), (40, 64, 2, 1030, 40), (40, 48, 2, 1100, 70), (40, 100, 2, 65, 70),
+           (3, 16, 11, 40, 24), (6, 16, 11, 40, 24), (2, 20, 17, 33, 20), (4, 20, 16, 33, 20)]
 
 
 @pytest.mark.parametrize("dtype,bits", DTYPES)

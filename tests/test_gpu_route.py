@@ -83,7 +83,7 @@ def logits(T, E, seed, std=1.0):
 
 SIZES = [(1, 1, 1), (5, 2, 2), (3, 5, 5), (7, 15, 4), (9, 16, 16), (33, 17, 3), (64, 63, 6), (130, 64, 6), (67, 65, 8),
          (9, 100, 7), (41, 128, 1), (19, 160, 8), (50, 256, 8), (3, 256, 9), (2, 256, 256), (17, 257, 8), (21, 384, 8),
-         (5, 512, 17), (6, 1000, 12), (3, 1024, 33), (4, 2500, 8), (2, 4096, 5)]
+         (5, 512, 17), (18, 512, 15), (5, 512, 16), (21, 64, 15), (21, 60, 16), (6, 1000, 12), (3, 1024, 33), (4, 2500, 8), (2, 4096, 5)]
 
 
 @pytest.mark.parametrize("T,E,K", SIZES)
