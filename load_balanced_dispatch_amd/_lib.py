@@ -362,7 +362,9 @@ def _launch(entry, *args, stream=None):
     for a in args:
         if a.__class__ is tuple:
             t, name, dtype, numel = a
-            # what every tensor after the first passes by, if nothing is wrong with it
+            if device is None and t.__class__ is _Tensor and t.is_cuda:
+                device = t.get_device()
+            # what every tensor passes by, if nothing is wrong with it
             if not (t.__class__ is _Tensor and t.dtype is dtype and t.numel() == numel and t.is_contiguous()
                     and t.get_device() == device):
                 _ptr(t, name, dtype, numel)
@@ -551,14 +553,19 @@ def moonep_few_workspace_bytes(d: Dims, H: int, Hp: int) -> int:
     return int(_LIB.moonep_few_workspace_bytes(d, int(H), int(Hp)))
 
 
-def _few(entry, d, H, Hp, G, X, topk_idx, gates, weights, out, wide, workspace, stream):
-    t, code = _row_type(X, "X")
-    if workspace is not None and workspace.numel() * workspace.element_size() < moonep_few_workspace_bytes(d, H, Hp):
-        raise ValueError(f"workspace too small: {moonep_few_workspace_bytes(d, H, Hp)} bytes needed")
+def _few(entry, d, H, Hp, G, row_type, X, topk_idx, gates, weights, out, wide, workspace, stream):
+    t, code = row_type
+    ws = (workspace, "workspace", None, None)
+    if workspace is not None:
+        n = workspace.numel()
+        if n * workspace.element_size() < _LIB.moonep_few_workspace_bytes(d, H, Hp):
+            raise ValueError(f"workspace too small: {moonep_few_workspace_bytes(d, H, Hp)} bytes needed")
+        ws = (workspace, "workspace", workspace.dtype, n)
     T, f32 = d.R * d.S, torch.float32
-    _launch(entry, d, int(H), int(Hp), *G, code, (X, "X", t, T * H), (topk_idx, "topk_idx", torch.int32, d.N),
-            _or_none(gates, "gates", f32, d.N), *weights, (out, "out", f32, T * wide),
-            (workspace, "workspace", None, None), stream=stream)
+    N = T * d.K
+    _launch(entry, d, H, Hp, *G, code, (X, "X", t, T * H), (topk_idx, "topk_idx", torch.int32, N),
+            None if gates is None else (gates, "gates", f32, N), *weights, (out, "out", f32, T * wide), ws,
+            stream=stream)
 
 
 def _weights4(codes, scales, E, H, N, G, name):
@@ -569,27 +576,29 @@ def _weights4(codes, scales, E, H, N, G, name):
 
 def moonep_few_layer(d: Dims, H: int, Hp: int, X, topk_idx, gates, W_home, out, workspace, stream=None):
     """One expert projection and the combine for few tokens, without a plan: out [R,S,Hp] float32."""
-    _few(_LIB.moonep_few_layer, d, H, Hp, (), X, topk_idx, gates,
-         ((W_home, "W_home", _row_type(X, "X")[0], d.E * H * Hp),), out, Hp, workspace, stream)
+    t = _row_type(X, "X")
+    _few(_LIB.moonep_few_layer, d, H, Hp, (), t, X, topk_idx, gates, ((W_home, "W_home", t[0], d.E * H * Hp),), out, Hp,
+         workspace, stream)
 
 
 def moonep_few_ffn(d: Dims, H: int, Hp: int, X, topk_idx, gates, W_gu, W_down, out, workspace, stream=None):
     """The whole gated expert layer for few tokens, without a plan: out [R,S,H] float32."""
-    t = _row_type(X, "X")[0]
-    _few(_LIB.moonep_few_ffn, d, H, Hp, (), X, topk_idx, gates,
-         ((W_gu, "W_gu", t, d.E * H * 2 * Hp), (W_down, "W_down", t, d.E * Hp * H)), out, H, workspace, stream)
+    t = _row_type(X, "X")
+    n = d.E * H * Hp
+    _few(_LIB.moonep_few_ffn, d, H, Hp, (), t, X, topk_idx, gates,
+         ((W_gu, "W_gu", t[0], 2 * n), (W_down, "W_down", t[0], n)), out, H, workspace, stream)
 
 
 def moonep_few_layer4(d: Dims, H: int, Hp: int, G: int, X, topk_idx, gates, codes, scales, out, workspace, stream=None):
     """moonep_few_layer with 4-bit weights."""
-    _few(_LIB.moonep_few_layer4, d, H, Hp, (int(G),), X, topk_idx, gates, _weights4(codes, scales, d.E, H, Hp, G, ""),
-         out, Hp, workspace, stream)
+    _few(_LIB.moonep_few_layer4, d, H, Hp, (G,), _row_type(X, "X"), X, topk_idx, gates,
+         _weights4(codes, scales, d.E, H, Hp, G, ""), out, Hp, workspace, stream)
 
 
 def moonep_few_ffn4(d: Dims, H: int, Hp: int, G: int, X, topk_idx, gates, gu_codes, gu_scales, down_codes, down_scales,
                     out, workspace, stream=None):
     """moonep_few_ffn with 4-bit weights."""
-    _few(_LIB.moonep_few_ffn4, d, H, Hp, (int(G),), X, topk_idx, gates,
+    _few(_LIB.moonep_few_ffn4, d, H, Hp, (G,), _row_type(X, "X"), X, topk_idx, gates,
          _weights4(gu_codes, gu_scales, d.E, H, 2 * Hp, G, "gu_") + _weights4(down_codes, down_scales, d.E, Hp, H, G,
                                                                                "down_"), out, H, workspace, stream)
 
