@@ -505,14 +505,16 @@ __device__ __forceinline__ void few_tile(const W& w, const R& rows, const O& out
   __syncthreads();
 }
 
-// Three operands a row would take a few registers more than let four waves share a SIMD: held to those, with a few
-// addresses spilled, 12 float32 rows through 16 experts of 1413 x 1531 in 4 bits 14.2 us (15.4 without; all pairs as packed
-// rows 17.0).
 template <class W, class R, class O, int MT, int NW, int KW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(R::Wide::S > 1 ? 4 : 2))) void few_mfma(W w, R rows, O out, Pairs pairs, int H, int C) {
+__global__ __launch_bounds__(NW * 64) void few_mfma(W w, R rows, O out, Pairs pairs, int H, int C) {
   typedef typename R::Wide Wide;
   constexpr int TW = 16 * W::kV, PT = kRows / Wide::kPer;
-  constexpr int U = O::kGated ? W::kGatedU : W::kPlainU, kWideU = U > 1 && Wide::S > 1 ? U / 2 : U;
+  // float32 rows, twice as long in registers, in half as many steps, and three operands in half of those: four waves then
+  // share a SIMD (12 rows through 16 experts of 1413 x 1531 in 4 bits: 12.7 us, 15.4 with as many steps, 17.0 with packed
+  // rows for all pairs)
+  constexpr bool kLong = Wide::S > 1;
+  constexpr int U0 = O::kGated ? W::kGatedU : W::kPlainU, U = U0 > 1 && kLong ? U0 / 2 : U0;
+  constexpr int kWideU = U > 1 && kLong ? U / 2 : U;
   extern __shared__ float lds[];  // sums [NW][kRows][TW], then the block's pairs
   int32_t* list = reinterpret_cast<int32_t*>(lds + NW * kRows * TW);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
