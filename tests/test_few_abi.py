@@ -143,6 +143,14 @@ def test_sizes_of_4_bit_weights():
         assert "dtype" in m.last_error()
 
 
+def test_grid_of_4_bit_weights():
+    # 8 waves to 128 rows and 256 columns: from 2^23 such tiles on the grid would have 2^32 threads
+    for name, call in FOUR.items():
+        for E, H, N in ((1 << 23, 8, 8), (1 << 22, 129, 8), (1 << 22, 8, 257), ((1 << 24) - 1, 8, 8)):
+            assert call(E, H, N, 32, BF, P[:3]) == _lib.MOONEP_EINVAL
+            assert "grid too large" in m.last_error() and name in m.last_error()
+
+
 def test_nothing_to_do_is_ok():
     d = m.make_dims(2, 4, 1, 0, 2)
     for call, n, *_ in FEW.values():
