@@ -460,7 +460,7 @@ typedef enum moonep_score {
  *   in descending order, the lowest id first among equals.
  *   gates = scale * s_e, or with renorm scale * s_e / (sum of the chosen experts' s); float32 arithmetic.
  *   A logit of NaN or -inf masks its expert: it has s = 0 and is never chosen, as one whose bias is NaN or -inf is not
- *   chosen.  +inf counts as the largest float.  A token with fewer than K experts to choose from has id -1 (which the
+ *   chosen.  +inf counts as the largest float, as a logit and as a bias.  A token with fewer than K experts to choose from has id -1 (which the
  *   other calls leave out) and gate 0 in the places that are left.
  * In:  logits [R,S,E] float32;  bias [E] float32 or NULL.
  * Out: topk_idx [R,S,K] int32;  gates [R,S,K] float32.

@@ -321,10 +321,12 @@ __global__ __launch_bounds__(kRowWaves * 64) void route_rows(const float* __rest
   bool doubt = NV > 4 && taken == 4;
   if constexpr (BIAS) {
     // Scores are at most 1 and off by at most 8 u (u = 2^-24; softmax: by the rounding of a sum of E more), a key by u of
-    // itself more: two keys that differ by less than twice that may be in another order.
+    // itself more: two keys that differ by less than twice that may be in another order.  An infinite key, of a bias that
+    // counts as the largest float, may be after another of those.
     const float near = (SIGMOID ? 24.f : (float)(E / 8 + 64)) * 0x1p-24f;
     const float v = from_order(at), before = from_order(dpp<0x111>(at));  // the lane before
-    doubt |= (l16 > 0) & (l16 <= K) & (at > kMasked) & !(before - v > near * fmaxf(1.f, fabsf(v)));
+    doubt |= (l16 > 0) & (l16 <= K) & (at > kMasked) &
+             (!(before - v > near * fmaxf(1.f, fabsf(v))) | (before > kLargest));
   }
   if (at <= kMasked || l16 >= K) id = -1;
   float chosen = id >= 0 ? from_order(at) : -INFINITY;  // without a bias the key is the logit

@@ -133,6 +133,18 @@ def test_masks_and_extremes(m, E):
         check(m, l[rows], bias, 6, score, renorm, 1.5)
 
 
+@pytest.mark.parametrize("E", [8, 64, 256, 300])
+def test_infinite_and_largest_biases_are_alike(m, E):
+    # both count as the largest float, so that the scores do not matter: the lowest index first
+    l = logits(9, E, seed=E)
+    bias = np.zeros(E, np.float32)
+    bias[1], bias[3], bias[E - 2] = few.LARGEST, np.inf, few.LARGEST
+    for score, renorm in KINDS:
+        for K in (1, 2, 3, 5):
+            ids, _ = check(m, l, bias, K, score, renorm, 1.0)
+            assert npi(ids)[:, :min(K, 3)].tolist() == [[1, 3, E - 2][:min(K, 3)]] * 9
+
+
 def test_backward_takes_any_ids(m):
     # ids outside [0, E) are left out, the same expert twice adds up, and so does a masked one's nothing
     T, E, K = 6, 40, 4
