@@ -512,6 +512,7 @@ int moonep_few_layer(moonep_dims d, int32_t H, int32_t Hp, moonep_dtype t, const
  * moonep_few_ffn -- the whole gated expert layer:
  *   out[r,s] = sum over k ascending of gates[r,s,k] * (A @ W_down[e]),  e = topk_idx[r,s,k],
  *   A = silu(X[r,s] @ W_gu[e][:, :Hp]) * (X[r,s] @ W_gu[e][:, Hp:]).
+ * An infinity in a bfloat16 W_down gives NaN, as A is multiplied in parts of which some are 0.
  * In:  X [R,S,H] dtype t;  topk_idx [R,S,K] int32;  gates [R,S,K] float32 or NULL (1);
  *      W_gu [E,H,2*Hp], W_down [E,Hp,H] dtype t.
  * Out: out [R,S,H] float32.

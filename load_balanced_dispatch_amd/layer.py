@@ -449,6 +449,9 @@ class MoeFew:
     def save_weights(self, W_gu, W_down):
         """Writes weights [E, H, 2H'] and [E, H', H] (bfloat16 or float32) as the layer keeps them."""
         E, H, Hp = self.d.E, self.H, self.Hp
+        for name, t, shape in (("W_gu", W_gu, (E, H, 2 * Hp)), ("W_down", W_down, (E, Hp, H))):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
         if self.bits == 4:
             _lib.moonep_save4(E, H, 2 * Hp, self.G, W_gu, self.gu_codes, self.gu_scales)
             _lib.moonep_save4(E, Hp, H, self.G, W_down, self.down_codes, self.down_scales)

@@ -70,3 +70,13 @@ def test_weights_are_copied_as_they_are():
     g, w = torch.randn(4, 64, 64), torch.randn(4, 32, 64)
     L.save_weights(g, w)
     assert torch.equal(L.W_gu, g) and torch.equal(L.W_down, w)
+
+
+def test_weights_of_another_shape_are_refused():
+    # copy_ alone would repeat one expert's for all, and save4 read a transposed tensor of as many elements
+    g, w = torch.randn(4, 64, 64), torch.randn(4, 32, 64)
+    for L in (m.MoeFew(*FEW, device="cpu"), m.MoeFew(*FEW, device="cpu", bits=4)):
+        with pytest.raises(ValueError, match="W_gu must be"):
+            L.save_weights(g[:1], w)
+        with pytest.raises(ValueError, match="W_down must be"):
+            L.save_weights(g, w.transpose(1, 2).contiguous())
