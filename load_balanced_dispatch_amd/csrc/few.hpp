@@ -171,7 +171,7 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 // element and no LDS.
 template <int V>
 struct WeightsBf16 {
-  static constexpr int kV = V, kGatedU = 2, kPlainU = 2;  // steps whose loads are in flight together
+  static constexpr int kV = V, kGatedU = 2, kPlainU = V > 2 ? 2 : 4;  // steps whose loads are in flight together
   const uint16_t* w;
   int H, N;
   struct Raw {
@@ -228,7 +228,7 @@ struct WeightsBf16 {
 // float32 weights: the float32 matrix instruction takes one row of a lane at a time.
 template <int V>
 struct WeightsF32 {
-  static constexpr int kV = V, kGatedU = 1, kPlainU = 2;
+  static constexpr int kV = V, kGatedU = V > 1 ? 1 : 2, kPlainU = V > 1 ? 2 : 4;
   const float* w;
   int H, N;
   struct Raw {
@@ -272,7 +272,7 @@ struct WeightsF32 {
 // at the row's product with -24.  The scale multiplies the float32 sum of 32 rows.
 template <int V>
 struct WeightsFour {
-  static constexpr int kV = V, kGatedU = 2, kPlainU = 4;
+  static constexpr int kV = V, kGatedU = V > 1 ? 2 : 4, kPlainU = 4;
   const uint32_t* codes;
   const uint16_t* scales;
   int H, N, G;
@@ -545,7 +545,7 @@ __global__ __launch_bounds__(NW * 64) void few_mfma(W w, R rows, O out, Pairs pa
     else if (MT == 1 || here <= PT)
       few_tile<W, Wide, O, 1, NW, KW, kWideU>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
     else
-      few_tile<W, Wide, O, MT, NW, KW, 1>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
+      few_tile<W, Wide, O, MT, NW, KW, W::kV <= 2 ? U0 / 2 : 1>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
   }
 }
 
@@ -630,6 +630,16 @@ inline bool by_token(const Call& c) {
   return c.d.K <= kManyWaves && c.T() <= 4 && (c.G ? n / 2 : n * (int64_t)elem_bytes(c.t)) <= (8 << 20);
 }
 
+// Whether tiles of the usual 64 columns would be so few that most of the chip has nothing to read while their blocks' waves
+// go down a long input: then tiles a half or a quarter as wide, with 16 waves to a tile and more of their steps in
+// flight.  24 tokens, 2 experts of 3503 x 141 in float32 23 us (49 with wide tiles), 3 tokens, 4 experts of 4288 x 896
+// 68 (93), 4 tokens, 8 experts of 5641 x 128 in bf16 15 (21), 4 tokens, one expert of 5120 x 64 and its way back in 4 bits
+// 23 (30); but in 4 bits, where each row's operand costs more than a column's, 8 tokens, 4 experts of 7167 x 1407 30 (26), and
+// short inputs gain nothing: 14 tokens, 6 experts of 64 x 512 14.8 (13.4).
+inline bool narrow(const Call& c, const Product& p) {
+  return steps_of(p.H) >= 24 && (int64_t)c.rows() * ceil_div_u(p.width, 64) < (c.G ? 64 : 128);
+}
+
 template <class W, class R, class O, int MT, int NW, int KW>
 void launch(const Call& c, const Product& p, W w, R rows, O out) {
   constexpr int TW = 16 * W::kV;
@@ -649,8 +659,11 @@ void launch(const Call& c, const Product& p, W w, R rows, O out) {
 
 template <class W, class R, class O>
 void by_expert(const Call& c, const Product& p, W w, R rows, O out) {
-  if constexpr (W::kV == 1) {
-    launch<W, R, O, 1, kWaves, 8>(c, p, w, rows, out);
+  constexpr int PT = kRows / R::Wide::kPer;
+  if constexpr (W::kV <= 2) {
+    if constexpr (R::Wide::S == 1)
+      if (c.T() > PT) return launch<W, R, O, 2, kManyWaves, kManyWaves>(c, p, w, rows, out);
+    launch<W, R, O, 1, kManyWaves, kManyWaves>(c, p, w, rows, out);
   } else {
     const int64_t tiles = (int64_t)c.rows() * ceil_div_u(p.width, 16 * W::kV);
     // Waves one after the other along the input rows: enough of them for the chip, and more while each keeps 20 steps
@@ -667,7 +680,6 @@ void by_expert(const Call& c, const Product& p, W w, R rows, O out) {
     };
     // Two instructions' rows side by side where more tokens than one holds could choose the same expert: twice the sums in
     // registers, but its weights read once (32 tokens, 256 experts: 1811 against 1835 us).  Three operands need no more.
-    constexpr int PT = kRows / R::Wide::kPer;
     if constexpr (R::Wide::S == 1)
       if (c.T() > PT) return with(std::integral_constant<int, 2>{});
     with(std::integral_constant<int, 1>{});

@@ -14,6 +14,7 @@ void last_bf16(const Call& c, const Product& p, const void* weights, R rows, flo
   const ToRows out{z, p.C};
   if (by_token(c) && p.C >= 2) by_tokens(c, p, WeightsBf16<2>{w, p.H, p.C}, rows);
   else if (by_token(c)) by_tokens(c, p, WeightsBf16<1>{w, p.H, p.C}, rows);
+  else if (p.C >= 2 && narrow(c, p)) by_expert(c, p, WeightsBf16<2>{w, p.H, p.C}, rows, out);
   else if (p.C >= 8 && waves >= 3072) by_expert(c, p, WeightsBf16<8>{w, p.H, p.C}, rows, out);
   else if (p.C >= 4) by_expert(c, p, WeightsBf16<4>{w, p.H, p.C}, rows, out);
   else by_expert(c, p, WeightsBf16<1>{w, p.H, p.C}, rows, out);
@@ -28,7 +29,8 @@ void run_bf16(const Call& c, void* act, float* z) {
   const uint16_t* w = static_cast<const uint16_t*>(c.w1);
   const Product one{c.d.K, c.H, c.Hp, wide, c.Hp % 64 == 0};
   const ToActParts a{parts, c.Hp, wide};
-  if (c.Hp >= 4) by_expert(c, one, WeightsBf16<4>{w, c.H, 2 * c.Hp}, x, a);
+  if (c.Hp >= 2 && narrow(c, one)) by_expert(c, one, WeightsBf16<2>{w, c.H, 2 * c.Hp}, x, a);
+  else if (c.Hp >= 4) by_expert(c, one, WeightsBf16<4>{w, c.H, 2 * c.Hp}, x, a);
   else by_expert(c, one, WeightsBf16<1>{w, c.H, 2 * c.Hp}, x, a);
   last_bf16(c, Product{1, c.Hp, c.H, c.H, c.H % 64 == 0}, c.w2, RowsParts{parts, wide}, z);
 }

@@ -440,3 +440,15 @@ def test_layer_through_save4(m):
         one = few.few_ffn(np64(X).reshape(T, H), ri[:, k:k + 1], rg[:, k:k + 1], *rows, 0.0)[0]
         bound = bound + (E + 40) * U * np.abs(one)
     assert np.all(np.abs(np64(out).reshape(T, H) - ref) <= bound)
+
+
+# T, E, K, H, Hp: long inputs with so few tiles that they are cut narrower, in either product; rows for one and for two
+# matrix instructions, few and many waves' steps, widths off the tiles' and down to one column
+NARROW = [(24, 2, 2, 3503, 141), (3, 4, 2, 769, 40), (5, 8, 3, 1536, 2), (4, 3, 1, 800, 1), (40, 3, 2, 33, 770),
+          (7, 16, 4, 1024, 65), (33, 2, 1, 775, 800), (9, 2, 2, 2080, 3)]
+
+
+@pytest.mark.parametrize("dtype,bits", DTYPES)
+@pytest.mark.parametrize("T,E,K,H,Hp", NARROW)
+def test_long_inputs_of_few_tiles(m, dtype, bits, T, E, K, H, Hp):
+    Case(m, T, E, K, H, Hp, dtype, bits, seed=T + H).check()
