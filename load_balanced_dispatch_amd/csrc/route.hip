@@ -570,7 +570,9 @@ void by_size(const Route& r, F f) {
   };
   if (r.d.E <= 64) kinds(std::integral_constant<int, 4>{});
   else if (r.d.E <= 128) kinds(std::integral_constant<int, 8>{});
+  else if (r.d.E <= 192) kinds(std::integral_constant<int, 12>{});
   else if (r.d.E <= 256) kinds(std::integral_constant<int, 16>{});
+  else if (r.d.E <= 384) kinds(std::integral_constant<int, 24>{});
   else kinds(std::integral_constant<int, 32>{});
 }
 
