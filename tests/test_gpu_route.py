@@ -133,6 +133,25 @@ def test_masks_and_extremes(m, E):
         check(m, l[rows], bias, 6, score, renorm, 1.5)
 
 
+@pytest.mark.parametrize("E", [128, 192, 256, 384, 512])
+def test_the_largest_lie_together(m, E):
+    # more of the largest keys than the sorted ones of a lane hold: columns 4 j .. 4 j + 3 of every 64, in any order,
+    # far above the others, a little above and below them, and next to each other within float32's error of a score
+    rng = np.random.default_rng(E)
+    T = 48
+    l = (rng.standard_normal((T, E)) * 0.01).astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    for t in range(T):
+        lane = rng.integers(0, 16)
+        cols = np.concatenate([64 * q + 4 * lane + np.arange(4) for q in range(E // 64)])
+        lift = [1.0, 0.02, 0.0][t % 3]
+        l[t, cols] = lift + rng.permutation(len(cols)) * [1e-2, 2.0 ** -22, 0.0, 2.0 ** -23][t % 4]
+    for score, renorm in KINDS:
+        for K in (3, 4, 5, 8, 15):
+            check(m, l, None, K, score, renorm, 1.0)
+            check(m, l, bias, K, score, renorm, 1.0)
+
+
 @pytest.mark.parametrize("E", [8, 64, 256, 300])
 def test_infinite_and_largest_biases_are_alike(m, E):
     # both count as the largest float, so that the scores do not matter: the lowest index first
