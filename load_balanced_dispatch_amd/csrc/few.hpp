@@ -171,7 +171,8 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 // element and no LDS.
 template <int V>
 struct WeightsBf16 {
-  static constexpr int kV = V, kGatedU = 2, kPlainU = V > 2 ? 2 : 4;  // steps whose loads are in flight together
+  static constexpr int kV = V, kGatedU = 2, kPlainU = V > 2 ? 2 : 4;  // steps in flight together: each kind's most
+                                                                       // that its registers hold
   const uint16_t* w;
   int H, N;
   struct Raw {
@@ -621,10 +622,10 @@ struct Product {
   bool lines;            // rows of weights are whole 128-byte lines
 };
 
-// Whether a token's block writes the sum of its pairs, without rows that are added up after it: where so few bytes are read
-// that the launch counts.  One token times a 7168 x 2048 matrix in 4 bits 9.9 us (14.3 through rows), 4 tokens through
-// the tiny float32 layer 12.4 (14.9); but the 235 MB of one token's down projections in the large layer 172 (134), and 8 tokens
-// of the mid layer in 4 bits 62 (53): its tiles are narrow, and experts that tokens share are read for each.
+// Whether a token's block writes the sum of its pairs, without rows that are added up after it: where so few bytes are
+// read that the launch counts.  One token times a 7168 x 2048 matrix in 4 bits 9 us (14.3 through rows), 4 tokens
+// through the tiny float32 layer 12 (14.9); but the 235 MB of one token's down projections in the large layer 172 (134),
+// and 8 tokens of the mid layer in 4 bits 62 (53): its tiles are narrow, and experts that tokens share are read for each.
 inline bool by_token(const Call& c) {
   const int64_t n = (int64_t)c.pairs() * c.H * c.Hp;
   return c.d.K <= kManyWaves && c.T() <= 4 && (c.G ? n / 2 : n * (int64_t)elem_bytes(c.t)) <= (8 << 20);
@@ -653,8 +654,8 @@ void launch(const Call& c, const Product& p, W w, R rows, O out) {
   // 1413 x 759: 41.3 us, 46.1 with neighbours apart).
   pairs.group = p.lines ? 1 : 4;
   const unsigned round = 8 * pairs.group;
-  hipLaunchKernelGGL(kernel, dim3(ceil_div_u((int64_t)pairs.tiles * pairs.rows, round) * round), dim3(NW * 64), lds, c.s, w,
-                     rows, out, pairs, p.H, p.C);
+  hipLaunchKernelGGL(kernel, dim3(ceil_div_u((int64_t)pairs.tiles * pairs.rows, round) * round), dim3(NW * 64), lds,
+                     c.s, w, rows, out, pairs, p.H, p.C);
 }
 
 template <class W, class R, class O>
@@ -668,8 +669,8 @@ void by_expert(const Call& c, const Product& p, W w, R rows, O out) {
     const int64_t tiles = (int64_t)c.rows() * ceil_div_u(p.width, 16 * W::kV);
     // Waves one after the other along the input rows: enough of them for the chip, and more while each keeps 20 steps
     // and they are not many times what the chip holds.  Measured against the other widths: one token through the large
-    // layer's gate and up 83 us with 8 (4: 120), 32 tokens 1190 with 4 (8: 1245); its down projections in 4 bits, 16 tokens,
-    // 157 with 2 (8: 190).
+    // layer's gate and up 83 us with 8 (4: 120), 32 tokens 1190 with 4 (8: 1245); its down projections in 4 bits, 16
+    // tokens, 157 with 2 (8: 190).
     int kw = 2;
     while (kw < 8 && (tiles * kw <= 1700 || (tiles * kw <= 20000 && steps_of(p.H) >= 20 * kw))) kw *= 2;
     auto with = [&](auto mt) {
@@ -691,7 +692,6 @@ void by_tokens(const Call& c, const Product& p, W w, R rows) {
   hipLaunchKernelGGL((few_tokens<W, R, kManyWaves>), dim3(ceil_div_u(p.C, 16 * W::kV), (unsigned)c.T()),
                      dim3(kManyWaves * 64), 0, c.s, w, rows, c.grid(p.per), c.gates, p.H, p.C, c.out);
 }
-
 
 // Enqueue all products of a call with weights of their kind; z: rows [pairs, H or Hp], act: the activation.
 void run_bf16(const Call& c, void* act, float* z);

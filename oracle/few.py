@@ -7,8 +7,8 @@ Router scores of a token's logits l: softmax(l) or sigmoid(l); NaN and -inf mask
 counts as the largest float32.  The K experts are the largest l, or with a bias the largest score + bias, descending, the
 lowest id first among equals; -1 (gate 0) where fewer are left.
 
-4-bit weights: per column and G rows, scale = bfloat16(float32(largest magnitude * float32(1/7))), code = the nearest whole number
-(ties to even) to the float32 quotient of value and scale, held within [-8, 7].
+4-bit weights: per column and G rows, scale = bfloat16(float32(largest magnitude * float32(1/7))), code = the nearest
+whole number (ties to even) to the float32 quotient of value and scale, held within [-8, 7].
 """
 from __future__ import annotations
 
