@@ -476,8 +476,9 @@ int moonep_route(moonep_dims d, int32_t score, int32_t renorm, float scale, cons
  *     sigmoid          dl_e = c_k * s_e * (1 - s_e) where e is chosen, 0 elsewhere
  *     softmax, renorm  dl_e = q_k * u_k             where e is chosen, 0 elsewhere
  *     sigmoid, renorm  dl_e = q_k * u_k * (1 - s_e) where e is chosen, 0 elsewhere
- *   float32 arithmetic.  Ids outside [0, E) are left out; a masked expert's gradient is 0.  The gradients of an id
- *   that a token holds more than once add up.
+ *   float32 arithmetic.  Ids outside [0, E) are left out; a masked expert's gradient is 0 whatever dgates holds, and with
+ *   softmax scores that of an expert whose s is 0 in float32.  The gradients of an id that a token holds more than once
+ *   add up.  E <= 4096, R*S <= 2^25.
  * In:  logits [R,S,E] float32;  topk_idx [R,S,K] int32 as moonep_route gives it;  dgates [R,S,K] float32.
  * Out: dlogits [R,S,E] float32 (all of it is written).
  */

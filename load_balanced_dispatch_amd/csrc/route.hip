@@ -431,7 +431,10 @@ __global__ __launch_bounds__(kRowWaves * 64) void route_back_rows(const float* _
     f32x4 d = mine[q * 16 + l16];
     if constexpr (kAll) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = x[4 * q + i] * over * (d[i] - inner);
+      for (int i = 0; i < 4; ++i) {  // an expert without a score has no part in an infinite or undefined inner sum
+        const float s = x[4 * q + i] * over;
+        d[i] = s > 0.f ? s * (d[i] - inner) : 0.f;
+      }
     }
     float* o = dlogits + t * E + e;
     if (e + 4 <= E) {
@@ -532,7 +535,10 @@ __global__ __launch_bounds__(64) void route_back_wave(const float* __restrict__ 
   __syncthreads();
   for (int e = lane; e < E; e += 64) {
     float v = row[e];
-    if (all) v = exp_f(logit(l[e]) - m) * over * (v - inner);
+    if (all) {
+      const float s = exp_f(logit(l[e]) - m) * over;
+      v = s > 0.f ? s * (v - inner) : 0.f;  // as in route_back_rows
+    }
     dlogits[t * E + e] = v;
   }
 }

@@ -111,7 +111,9 @@ def route_backward(logits, ids, dgates, score: str, renorm: bool, scale: float):
         z = np.abs(v)
     else:
         v, z = sk * c, sk * np.abs(c)
-        dl -= s * (sk * c).sum(axis=1, keepdims=True)
+        # an expert without a score has no part in an infinite or undefined sum
+        with np.errstate(invalid="ignore"):
+            dl -= np.where(s > 0, s * (sk * c).sum(axis=1, keepdims=True), 0.0)
         size += s * (sk * np.abs(c)).sum(axis=1, keepdims=True)
     for t, k in zip(*np.nonzero(on)):
         dl[t, ids[t, k]] += v[t, k]
