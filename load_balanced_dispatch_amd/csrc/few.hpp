@@ -173,6 +173,7 @@ template <int V>
 struct WeightsBf16 {
   static constexpr int kV = V, kGatedU = 2, kPlainU = V > 2 ? 2 : 4;  // steps in flight together: each kind's most
                                                                        // that its registers hold
+  static constexpr float kUnit = 1.f;  // what the sums of products are in units of
   const uint16_t* w;
   int H, N;
   struct Raw {
@@ -230,6 +231,7 @@ struct WeightsBf16 {
 template <int V>
 struct WeightsF32 {
   static constexpr int kV = V, kGatedU = V > 1 ? 1 : 2, kPlainU = V > 1 ? 2 : 4;
+  static constexpr float kUnit = 1.f;
   const float* w;
   int H, N;
   struct Raw {
@@ -270,10 +272,13 @@ struct WeightsF32 {
 
 // 4-bit weights: a word is the eight rows of one column.  A code takes the top mantissa bits of 16, so that the operand
 // is code + 24; what is too much, 24 times the sum of the row, is taken off by the same instruction, whose sum starts
-// at the row's product with -24.  The scale multiplies the float32 sum of 32 rows.
+// at the row's product with -24.  The scale multiplies the float32 sum of 32 rows.  So these sums round by float32 steps
+// of up to 56 scales times the row's values, whatever their codes.  Operands are in units of 2^-10, which
+// the whole sum is multiplied by in the end: 32 rows times at most 31 then stay within float32 for any finite row.
 template <int V>
 struct WeightsFour {
   static constexpr int kV = V, kGatedU = V > 1 ? 2 : 4, kPlainU = 4;
+  static constexpr float kUnit = 1024.f;
   const uint32_t* codes;
   const uint16_t* scales;
   int H, N, G;
@@ -310,7 +315,7 @@ struct WeightsFour {
   static __device__ __forceinline__ void mac(f32x4 (&acc)[MT][V], const Raw& r, const typename R::Raw (&x)[MT]) {
     bf16x8 a[MT][R::S];
     f32x4 start[MT];
-    const bf16x8 less = as_operand((u32x4)(0xc1c0c1c0u));  // -24
+    const bf16x8 less = as_operand((u32x4)(0xbcc0bcc0u));  // -24 / 1024
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       R::operands(x[t], a[t]);
@@ -321,8 +326,8 @@ struct WeightsFour {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const uint32_t w = r.d[j];
-      const u32x4 q = {(w << 3 & 0x00780078u) | 0x41804180u, (w >> 1 & 0x00780078u) | 0x41804180u,
-                       (w >> 5 & 0x00780078u) | 0x41804180u, (w >> 9 & 0x00780078u) | 0x41804180u};
+      const u32x4 q = {(w << 3 & 0x00780078u) | 0x3c803c80u, (w >> 1 & 0x00780078u) | 0x3c803c80u,
+                       (w >> 5 & 0x00780078u) | 0x3c803c80u, (w >> 9 & 0x00780078u) | 0x3c803c80u};
       const bf16x8 b = as_operand(q);
       const float scale = __uint_as_float(j % 2 ? r.s[j / 2] & 0xffff0000u : r.s[j / 2] << 16);
 #pragma unroll
@@ -491,6 +496,7 @@ __device__ __forceinline__ void few_tile(const W& w, const R& rows, const O& out
           for (int v = 0; v < KW; ++v)
 #pragma unroll
             for (int p = 0; p < kPer; ++p) sum[g][n] += mine[(v * kRows + q * kPer + p) * TW + i % TW];
+          sum[g][n] *= W::kUnit;
         }
       }
     }
@@ -587,7 +593,7 @@ __global__ __launch_bounds__(NW * 64) void few_tokens(W w, R rows, Pairs pairs, 
     if (id < 0 || id >= pairs.E) continue;
     float v = sums[q * each][i];
     for (int n = 1; n < each; ++n) v += sums[q * each + n][i];
-    a = __builtin_fmaf(gates != nullptr ? gates[t * K + q] : 1.f, v, a);
+    a = __builtin_fmaf(gates != nullptr ? gates[t * K + q] : 1.f, v * W::kUnit, a);
   }
   out[(int64_t)t * C + c0 + i] = a;
 }
