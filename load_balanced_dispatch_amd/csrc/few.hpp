@@ -6,8 +6,9 @@
 // after the other along the input rows, whose sums they add through LDS in a fixed order.  few_tokens takes a token and a
 // tile of columns to a block, its waves sharing the token's experts and their rows, and writes the token's whole sum.
 //
-// Everything is exact to float32: bf16 weights are operands as they are, activations are split into three bf16 parts that
-// hold all of their 24 bits, and the products of bf16 numbers are exact in a float32 sum.
+// Nothing is rounded below float32: bf16 weights are operands as they are, float32 activations are split into three bf16
+// parts that hold all of their 24 bits, and the products of bf16 numbers are exact in a float32 sum.  Sums round by the
+// size of their terms; with 4-bit weights by that of up to 56 scales times the activation (WeightsFour).
 //
 // HBM bounds it where experts are many or large (32 tokens, 256 experts of 7168 x 2048, 120 of them chosen: 10.6 GB at 5.7
 // TB/s; in 4 bits, 16 tokens, 80 experts: 2.0 GB at 5 TB/s); one token keeps few blocks busy, of which a CU draws at most

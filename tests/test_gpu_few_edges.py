@@ -101,3 +101,29 @@ def test_ffn4_with_activations_of_any_size(m, dtype, T, E, K, H, Hp):
         err = np.abs(out.view.double().cpu().numpy() - ref)
         assert np.all(err <= bound + 2.0 ** -100), b
         assert out.intact() and ws.intact()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 6, 12])
+def test_an_outlier_on_zero_codes(m, dtype, T):
+    # a row's value that only meets the code 0 is still added, and taken off: what it leaves is within the stated bound
+    E, H, Hp, G, K = 1, 64, 48, 32, 1
+    d = m.make_dims(1, E, 0, T, K)
+    codes = np.random.default_rng(0).integers(-8, 8, (E, H, Hp))
+    codes[:, 5] = codes[:, 40] = 0
+    scales = np.full((E, H // G, Hp), 0.5)
+    words, s = torch.as_tensor(few.pack4(codes)).to(DEV), torch.tensor(scales, dtype=F32).to(BF).to(DEV)
+    values, ids, gates = few.load4(codes, scales, G), np.zeros((T, K), np.int64), np.ones((T, K), np.float32)
+    for b in (4, 8, 16, 24, 40):
+        X = rand_tensor((T, H), dtype, 8)
+        X[:, 5], X[:, 40] = 2.0 ** b, -1.5 * 2.0 ** b
+        out, ws = Guarded((T, Hp), F32), space(m, d, H, Hp)
+        say("few_layer4 outlier 2 ^", b, dtype, T)
+        m.moonep_few_layer4(d, H, Hp, G, X, i32(ids), None, words, s, out.view, ws.view)
+        torch.cuda.synchronize()
+        x = X.double().cpu().numpy()
+        ref, _ = few.few_layer(x, ids, gates, values)
+        bound = 2 * (H + K + 16) * U * 56 * 0.5 * np.abs(x).sum(1, keepdims=True)
+        err = np.abs(out.view.double().cpu().numpy() - ref)
+        assert np.all(err <= bound), (b, float((err / bound).max()))
+        assert out.intact() and ws.intact()
