@@ -175,6 +175,7 @@ struct WeightsBf16 {
   static constexpr int kV = V, kGatedU = 2, kPlainU = V > 2 ? 2 : 4;  // steps in flight together: each kind's most
                                                                        // that its registers hold
   static constexpr float kUnit = 1.f;  // what the sums of products are in units of
+  static constexpr int kBytes = 2;  // of one column of a load
   const uint16_t* w;
   int H, N;
   struct Raw {
@@ -233,6 +234,7 @@ template <int V>
 struct WeightsF32 {
   static constexpr int kV = V, kGatedU = V > 1 ? 1 : 2, kPlainU = V > 1 ? 2 : 4;
   static constexpr float kUnit = 1.f;
+  static constexpr int kBytes = 4;
   const float* w;
   int H, N;
   struct Raw {
@@ -280,6 +282,7 @@ template <int V>
 struct WeightsFour {
   static constexpr int kV = V, kGatedU = V > 1 ? 2 : 4, kPlainU = 4;
   static constexpr float kUnit = 1024.f;
+  static constexpr int kBytes = 4;
   const uint32_t* codes;
   const uint16_t* scales;
   int H, N, G;
@@ -657,9 +660,11 @@ void launch(const Call& c, const Product& p, W w, R rows, O out) {
     (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   Pairs pairs = c.grid(p.per);
   pairs.tiles = ceil_div_u(p.width, TW * (NW / KW)), pairs.rows = c.rows();
-  // Where tiles share lines, neighbours go to one XCD, whose L2 then reads those once (15 tokens, 21 experts of
-  // 1413 x 759: 41.3 us, 46.1 with neighbours apart).
-  pairs.group = p.lines ? 1 : 4;
+  // Where tiles share lines, since rows or tiles are no whole ones, neighbours go to one XCD, whose L2 then reads those
+  // once (15 tokens, 21 experts of 1413 x 759: 41.3 us, 46.1 with neighbours apart; narrow tiles, 3 tokens, 4 float32 experts
+  // of 4288 x 896: 54.2, and 59.4 apart).  Others go apart (32 tokens, 64 float32 experts of 2048 x 1408: 357 us, 361 with
+  // neighbours on one XCD).
+  pairs.group = p.lines && TW * W::kBytes % 128 == 0 ? 1 : 4;
   const unsigned round = 8 * pairs.group;
   hipLaunchKernelGGL(kernel, dim3(ceil_div_u((int64_t)pairs.tiles * pairs.rows, round) * round), dim3(NW * 64), lds,
                      c.s, w, rows, out, pairs, p.H, p.C);
