@@ -127,3 +127,86 @@ def test_an_outlier_on_zero_codes(m, dtype, T):
         err = np.abs(out.view.double().cpu().numpy() - ref)
         assert np.all(err <= bound), (b, float((err / bound).max()))
         assert out.intact() and ws.intact()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H,Hp", [(6, 37, 20), (40, 37, 130), (7, 803, 20), (6, 803, 200)])
+def test_infinite_weights_in_an_experts_block(m, dtype, T, H, Hp):
+    # rows past the end are not multiplied: an infinity in the last row of an odd width stays one
+    E, K = 3, 2
+    d = m.make_dims(1, E, 0, T, K)
+    ids, gates = routing(T, E, K, 9)
+    w = rand_tensor((E, H, Hp), dtype, 10, H ** -0.5)
+    w[:, -1, 3] = float("inf")
+    X = rand_tensor((T, H), dtype, 11)
+    X[:, -1] = X[:, -1].abs() + 0.5
+    out, ws = Guarded((T, Hp), F32), space(m, d, H, Hp)
+    say("few_layer infinite weights", dtype, T, H, Hp)
+    m.moonep_few_layer(d, H, Hp, X, i32(ids), f32(gates), w, out.view, ws.view)
+    torch.cuda.synchronize()
+    assert torch.isposinf(out.view[:, 3]).all()
+    assert torch.isfinite(out.view[:, [i for i in range(Hp) if i != 3]]).all()
+    assert out.intact() and ws.intact()
+
+
+def test_words_and_scales_of_4_bits_past_32_bits(m):
+    """The last experts of more than 2^33 words and 2^31 scales."""
+    E, H, Hp, G, T, K = 2400, 7168, 4096, 32, 6, 2
+    assert E * (H // 8) * Hp > 2 ** 33 and E * (H // G) * Hp > 2 ** 31
+    d = m.make_dims(1, E, 0, T, K)
+    ids = np.array([[E - 1, 0], [E - 2, E - 1], [0, E - 2], [E - 1, E - 2], [E - 2, 0], [0, E - 1]])
+    gates = routing(T, E, K, 12)[1]
+    words = torch.empty((E, H // 8, Hp), dtype=torch.int32, device=DEV)
+    scales = torch.empty((E, H // G, Hp), dtype=BF, device=DEV)
+    values = {}
+    for e in (0, E - 2, E - 1):
+        v = torch.empty((1, H, Hp), device=DEV)
+        say("weights of expert", e)
+        m.moonep_save4(1, H, Hp, G, rand_tensor((1, H, Hp), BF, e, H ** -0.5), words[e:e + 1], scales[e:e + 1])
+        m.moonep_load4(1, H, Hp, G, words[e:e + 1], scales[e:e + 1], v)
+        values[e] = v[0].double()
+    X = rand_tensor((T, H), BF, 13)
+    for rows in (T, 1):  # an expert's block, and a token's
+        dr = m.make_dims(1, E, 0, rows, K)
+        out, ws = Guarded((rows, Hp), F32), space(m, dr, H, Hp)
+        say("few_layer4 past 2^33 words", rows)
+        m.moonep_few_layer4(dr, H, Hp, G, X[:rows], i32(ids[:rows]), f32(gates[:rows]), words, scales, out.view, ws.view)
+        torch.cuda.synchronize()
+        for t in range(rows):
+            terms = [(float(gates[t, k]), values[int(ids[t, k])]) for k in range(K)]
+            ref = sum(g * (X[t].double() @ w) for g, w in terms)
+            size = sum(g * (X[t].double().abs() @ w.abs()) for g, w in terms)
+            # a wrong expert or scale is off by the size of the terms, of which the roundings are far below a thousandth
+            assert float(((out.view[t].double() - ref).abs() / size).max()) < 1e-3
+        assert out.intact() and ws.intact()
+
+
+def test_save4_and_load4_past_32_bits(m):
+    """Expert offsets past 2^31 words and 2^34 weights, within one call."""
+    E, H, N, G = 2100, 2048, 4096, 64
+    assert E * H * N > 2 ** 34 and E * (H // 8) * N > 2 ** 31
+    few_experts = (0, 1049, E - 1)
+    W = torch.zeros((E, H, N), dtype=BF, device=DEV)
+    for e in few_experts:
+        W[e] = rand_tensor((H, N), BF, e, 0.1)
+    words = torch.empty((E, H // 8, N), dtype=torch.int32, device=DEV)
+    scales = torch.empty((E, H // G, N), dtype=BF, device=DEV)
+    say("save4 past 2^31 words")
+    m.moonep_save4(E, H, N, G, W, words, scales)
+    torch.cuda.synchronize()
+    kept = {}
+    for e in few_experts:
+        one = torch.empty((1, H // 8, N), dtype=torch.int32, device=DEV), torch.empty((1, H // G, N), dtype=BF, device=DEV)
+        m.moonep_save4(1, H, N, G, W[e:e + 1].clone(), *one)
+        torch.cuda.synchronize()
+        assert torch.equal(words[e], one[0][0]) and torch.equal(scales[e], one[1][0])
+        kept[e] = torch.empty((1, H, N), dtype=BF, device=DEV)
+        m.moonep_load4(1, H, N, G, *one, kept[e])
+    assert not scales[E - 2].any() and torch.equal(words[E - 2], words[1])
+    W.fill_(1.0)
+    say("load4 past 2^31 words")
+    m.moonep_load4(E, H, N, G, words, scales, W)
+    torch.cuda.synchronize()
+    for e in few_experts:
+        assert torch.equal(W[e], kept[e][0])
+    assert not W[E - 2].any() and not W[1].any()
