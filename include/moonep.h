@@ -488,11 +488,13 @@ int moonep_route_backward(moonep_dims d, int32_t score, int32_t renorm, float sc
 /*
  * The layer for few tokens (decoding).  With a handful of tokens the time goes into reading the chosen experts'
  * weights, and a plan, slots and row buffers have nothing to balance: these calls take topk_idx and gates as they are,
- * read each chosen expert's home weights once and need no plan.  They take R*S*K <= MOONEP_FEW_PAIRS pairs
- * (MOONEP_EINVAL beyond: the planned calls are for those), H and Hp up to 65536, and use of d only R, E, S and K.
- * Products and sums are float32 and nothing is rounded to dtype t on the way.  Pairs whose id is outside [0, E) are
- * left out; an expert that a token holds twice counts twice.  Results are the same from call to call.  Pointers need the
- * alignment of their elements only.
+ * read the chosen experts' home weights where they lie and need no plan.  One read of an expert's weights serves 16 of
+ * its pairs or more, in the down projection of bf16 and 4-bit weights 10 (5 with at most 5 tokens); with at most 4 tokens
+ * and a few MB of weights, a single pair.  The calls take R*S*K <= MOONEP_FEW_PAIRS pairs (MOONEP_EINVAL beyond: the
+ * planned calls are for those), H and Hp up to 65536, and use of d only R, E, S and K.  Products and sums are float32
+ * and nothing is rounded to dtype t on the way.  Pairs whose id is outside [0, E) are left out; an expert that a token
+ * holds twice counts twice.  Results are the same from call to call.  Pointers need the alignment of their elements
+ * only.  Output arrays overlap neither inputs nor the workspace.
  */
 enum { MOONEP_FEW_PAIRS = 1024 };
 

@@ -394,9 +394,9 @@ def _route_calls(layer):
 class MoeFew:
     """Static buffers for one gated expert layer that serves few tokens (R*S*K <= MOONEP_FEW_PAIRS), and its calls.
 
-    forward() writes out [R, S, H] (float32) from X [R, S, H], topk_idx and gates, without a plan: each chosen expert's
-    weights are read once.  `router`, `renorm`, `route_scale`, `router_bias`: as in MoeFFN, topk_idx and gates are then
-    made from `logits`.  `norm=True` puts the layer norm of MoeFFN in front (gamma, beta, eps; its rows, rounded to
+    forward() writes out [R, S, H] (float32) from X [R, S, H], topk_idx and gates, without a plan: the chosen experts'
+    weights are read where they lie, once for up to ten pairs of an expert (moonep_few_ffn has the numbers).  `router`,
+    `renorm`, `route_scale`, `router_bias`: as in MoeFFN, topk_idx and gates are then made from `logits`.  `norm=True` puts the layer norm of MoeFFN in front (gamma, beta, eps; its rows, rounded to
     dtype, are in Xn).
 
     The weights are the home weights of MoeFFN, W_gu [E, H, 2H'] and W_down [E, H', H] of `dtype`, or with bits=4 their
