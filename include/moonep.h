@@ -460,11 +460,13 @@ typedef enum moonep_score {
  *   in descending order, the lowest id first among equals.
  *   gates = scale * s_e, or with renorm scale * s_e / (sum of the chosen experts' s); float32 arithmetic.
  *   A logit of NaN or -inf masks its expert: it has s = 0 and is never chosen, as one whose bias is NaN or -inf is not
- *   chosen.  +inf counts as the largest float, as a logit and as a bias.  A token with fewer than K experts to choose from has id -1 (which the
- *   other calls leave out) and gate 0 in the places that are left.
+ *   chosen.  +inf counts as the largest float, as a logit and as a bias.  A token with fewer than K experts to choose
+ *   from has id -1 (which the other calls leave out) and gate 0 in the places that are left.
+ *   Logits without a bias are compared as they are.  With a bias, and where many logits are equal, tokens whose choice
+ *   float32 does not settle are gone over again in float64: up to four times the time of well separated ones.
  * In:  logits [R,S,E] float32;  bias [E] float32 or NULL.
  * Out: topk_idx [R,S,K] int32;  gates [R,S,K] float32.
- * E <= 4096, R*S <= 2^25; B is not used.
+ * E <= 4096, R*S <= 2^25; B is not used.  Output arrays overlap neither inputs nor each other, here and in the gradient.
  */
 int moonep_route(moonep_dims d, int32_t score, int32_t renorm, float scale, const float* logits, const float* bias,
                  int32_t* topk_idx, float* gates, moonep_stream stream);
@@ -538,7 +540,8 @@ int moonep_few_ffn(moonep_dims d, int32_t H, int32_t Hp, moonep_dtype t, const v
  *   code = value / scale rounded to the nearest even whole number, held within [-8, 7] (0 where the scale is 0).
  *   A group with an infinity or a NaN has the scale NaN.
  * moonep_load4 -- the values that 4-bit weights stand for (float32: exactly; bf16: rounded once).
- * In/Out: W [E,H,N] dtype t;  codes, scales as above.  E >= 0; H, N up to 65536.
+ * In/Out: W [E,H,N] dtype t;  codes, scales as above, not overlapping W.  E >= 0; H, N up to 65536;
+ *   E * ceil(H/128) * ceil(N/256) < 2^23 (MOONEP_EINVAL beyond: several calls, some of the experts each).
  */
 int moonep_save4(int32_t E, int32_t H, int32_t N, int32_t G, moonep_dtype t, const void* W, int32_t* codes,
                  uint16_t* scales, moonep_stream stream);
