@@ -10,10 +10,9 @@
 // parts that hold all of their 24 bits, and the products of bf16 numbers are exact in a float32 sum.  Sums round by the
 // size of their terms; with 4-bit weights by that of up to 56 scales times the activation (WeightsFour).
 //
-// HBM bounds it where experts are many or large (32 tokens, 256 experts of 7168 x 2048, 120 of them chosen: 10.6 GB at 5.7
-// TB/s; in 4 bits, 16 tokens, 80 experts: 2.0 GB at 5 TB/s); one token keeps few blocks busy, of which a CU draws at most
-// about 40 GB/s (0.70 GB in 134 us, 5.3 TB/s); with a few MB the launches, 3 us each, and the latencies of one short chain
-// of loads and two barriers are what is left.
+// HBM bounds it where experts are many or large (32 tokens, 256 experts of 7168 x 2048, 120 of them chosen: 10.6 GB at
+// 5.7 TB/s; in 4 bits, 16 tokens, 80 experts: 2.0 GB at 5 TB/s; one token, eight experts: 0.70 GB at 5.3 TB/s).  With a
+// few MB the launches, 3 us each, and the latencies of one short chain of loads and two barriers are what is left.
 #pragma once
 
 #include <type_traits>
@@ -558,7 +557,8 @@ __global__ __launch_bounds__(NW * 64) void few_mfma(W w, R rows, O out, Pairs pa
     else if (MT == 1 || here <= PT)
       few_tile<W, Wide, O, 1, NW, KW, kWideU>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
     else
-      few_tile<W, Wide, O, MT, NW, KW, W::kV <= 2 ? U0 / 2 : 1>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0, here, tile);
+      few_tile<W, Wide, O, MT, NW, KW, W::kV <= 2 ? U0 / 2 : 1>(w, rows.wide(), out, pairs.per, H, C, e, lds, list + m0,
+                                                                here, tile);
   }
 }
 
@@ -646,9 +646,9 @@ inline bool by_token(const Call& c) {
 // Whether tiles of the usual 64 columns would be so few that most of the chip has nothing to read while their blocks' waves
 // go down a long input: then tiles a half or a quarter as wide, with 16 waves to a tile and more of their steps in
 // flight.  24 tokens, 2 experts of 3503 x 141 in float32 23 us (49 with wide tiles), 3 tokens, 4 experts of 4288 x 896
-// 68 (93), 4 tokens, 8 experts of 5641 x 128 in bf16 15 (21), 4 tokens, one expert of 5120 x 64 and its way back in 4 bits
-// 23 (30); but in 4 bits, where each row's operand costs more than a column's, 8 tokens, 4 experts of 7167 x 1407 30 (26), and
-// short inputs gain nothing: 14 tokens, 6 experts of 64 x 512 14.8 (13.4).
+// 68 (93), 4 tokens, 8 experts of 5641 x 128 in bf16 15 (21), 4 tokens, one expert of 5120 x 64 and its way back in
+// 4 bits 23 (30); but in 4 bits, where each row's operand costs more than a column's, 8 tokens, 4 experts of
+// 7167 x 1407 30 (26), and short inputs gain nothing: 14 tokens, 6 experts of 64 x 512 14.8 (13.4).
 inline bool narrow(const Call& c, const Product& p) {
   return steps_of(p.H) >= 24 && (int64_t)c.rows() * ceil_div_u(p.width, 64) < (c.G ? 64 : 128);
 }
@@ -659,13 +659,14 @@ void launch(const Call& c, const Product& p, W w, R rows, O out) {
   const size_t lds = (size_t)NW * kRows * TW * sizeof(float) + c.pairs() * sizeof(int32_t);
   auto kernel = few_mfma<W, R, O, MT, NW, KW>;
   if (lds > 65536)
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)lds);
   Pairs pairs = c.grid(p.per);
   pairs.tiles = ceil_div_u(p.width, TW * (NW / KW)), pairs.rows = c.rows();
   // Where tiles share lines, since rows or tiles are no whole ones, neighbours go to one XCD, whose L2 then reads those
-  // once (15 tokens, 21 experts of 1413 x 759: 41.3 us, 46.1 with neighbours apart; narrow tiles, 3 tokens, 4 float32 experts
-  // of 4288 x 896: 54.2, and 59.4 apart).  Others go apart (32 tokens, 64 float32 experts of 2048 x 1408: 357 us, 361 with
-  // neighbours on one XCD).
+  // once (15 tokens, 21 experts of 1413 x 759: 41.3 us, 46.1 with neighbours apart; narrow tiles, 3 tokens, 4 float32
+  // experts of 4288 x 896: 54.2, and 59.4 apart).  Others go apart (32 tokens, 64 float32 experts of 2048 x 1408: 357 us,
+  // 361 with neighbours on one XCD).
   pairs.group = p.lines && TW * W::kBytes % 128 == 0 ? 1 : 4;
   const unsigned round = 8 * pairs.group;
   hipLaunchKernelGGL(kernel, dim3(ceil_div_u((int64_t)pairs.tiles * pairs.rows, round) * round), dim3(NW * 64), lds,

@@ -10,12 +10,12 @@ void last_bf16(const Call& c, const Product& p, const void* weights, R rows, flo
   const uint16_t* w = static_cast<const uint16_t*>(weights);
   // 8 columns to a lane where there are enough tiles of them: 32 tokens through the large layer's down projections 620 us
   // (4 columns: 635), but 15 tokens through 21 experts of 759 x 1413 51 us with them and 46 with 4.
-  const int64_t waves = (int64_t)c.rows() * ceil_div_u(p.C, 128) * kWaves;
+  const int64_t tiles = (int64_t)c.rows() * ceil_div_u(p.C, 128);
   const ToRows out{z, p.C};
   if (by_token(c) && p.C >= 2) by_tokens(c, p, WeightsBf16<2>{w, p.H, p.C}, rows);
   else if (by_token(c)) by_tokens(c, p, WeightsBf16<1>{w, p.H, p.C}, rows);
   else if (p.C >= 2 && narrow(c, p)) by_expert(c, p, WeightsBf16<2>{w, p.H, p.C}, rows, out);
-  else if (p.C >= 8 && waves >= 3072) by_expert(c, p, WeightsBf16<8>{w, p.H, p.C}, rows, out);
+  else if (p.C >= 8 && tiles >= 384) by_expert(c, p, WeightsBf16<8>{w, p.H, p.C}, rows, out);
   else if (p.C >= 4) by_expert(c, p, WeightsBf16<4>{w, p.H, p.C}, rows, out);
   else by_expert(c, p, WeightsBf16<1>{w, p.H, p.C}, rows, out);
 }

@@ -196,9 +196,7 @@ __global__ __launch_bounds__(kWaves4 * 64) void load4_tiles(const int32_t* __res
   Four<uint16_t> s;
   s.load(scales + (at.e * groups + at.h / G) * N + at.c, at.n);
   T* out = W + (at.e * H + at.h) * N + at.c;
-#pragma unroll
-  for (int r = 0; r < kRows4; ++r) {
-    if (r >= rows) break;
+  for (int r = 0; r < min(kRows4, rows); ++r) {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)code4(word[r / 8][i], r % 8) * __uint_as_float(s.bits(i));
