@@ -645,9 +645,9 @@ inline bool by_token(const Call& c) {
 
 // Whether tiles of the usual 64 columns would be so few that most of the chip has nothing to read while their blocks' waves
 // go down a long input: then tiles a half or a quarter as wide, with 16 waves to a tile and more of their steps in
-// flight.  24 tokens, 2 experts of 3503 x 141 in float32 23 us (49 with wide tiles), 3 tokens, 4 experts of 4288 x 896
-// 68 (93), 4 tokens, 8 experts of 5641 x 128 in bf16 15 (21), 4 tokens, one expert of 5120 x 64 and its way back in
-// 4 bits 23 (30); but in 4 bits, where each row's operand costs more than a column's, 8 tokens, 4 experts of
+// flight.  24 tokens through one projection by 2 float32 experts of 3503 x 141 23 us (49 with wide tiles), 3 tokens
+// through the layer of 4 float32 experts of 4288 x 896 54 (93), 4 tokens through a projection by 8 bf16 experts of
+// 5641 x 128 15 (20), 4 tokens through the layer of one expert of 5120 x 64 in 4 bits 16 (26); but in 4 bits, where each row's operand costs more than a column's, 8 tokens, 4 experts of
 // 7167 x 1407 30 (26), and short inputs gain nothing: 14 tokens, 6 experts of 64 x 512 14.8 (13.4).
 inline bool narrow(const Call& c, const Product& p) {
   return steps_of(p.H) >= 24 && (int64_t)c.rows() * ceil_div_u(p.width, 64) < (c.G ? 64 : 128);
