@@ -554,7 +554,8 @@ int moonep_load4(int32_t E, int32_t H, int32_t N, int32_t G, moonep_dtype t, con
  *   rows with one 4-bit matrix.  dtype t is X's.  Finite values of any size; infinities in X or in the activation give NaN.
  *   32 rows are added up as x * (code + 24) less 24 * x, in float32: whatever the codes, a product rounds like one whose
  *   terms are of the size 56 * scale * |x|, and is off by less than 2 (H + K + 16) 2^-24 of their sum.  A value that is
- *   much larger than its row's others and meets the code 0 leaves that much.
+ *   much larger than its row's others and meets the code 0 leaves that much.  Sums are kept to 2^-139, and to 2^-139 times
+ *   the scale, so that tiny rows and results have fewer places.  moonep_save4 makes W_gu for Hp up to 32768.
  */
 int moonep_few_layer4(moonep_dims d, int32_t H, int32_t Hp, int32_t G, moonep_dtype t, const void* X,
                       const int32_t* topk_idx, const float* gates, const int32_t* codes, const uint16_t* scales,

@@ -210,3 +210,53 @@ def test_save4_and_load4_past_32_bits(m):
     for e in few_experts:
         assert torch.equal(W[e], kept[e][0])
     assert not W[E - 2].any() and not W[1].any()
+
+
+@pytest.mark.parametrize("T", [6, 40])
+def test_wide_tiles_captured(m, T):
+    # eight columns to a lane: sums in more than 64 KB of LDS, which the launch asks for while a graph is captured too
+    E, K, H, Hp = 8, 2, 96, 6200
+    d = m.make_dims(1, E, 0, T, K)
+    w = rand_tensor((E, H, Hp), BF, 20, H ** -0.5)
+    X, ids, gates = rand_tensor((T, H), BF, 21), i32(routing(T, E, K, 22)[0]), f32(routing(T, E, K, 22)[1])
+    out, ws = Guarded((T, Hp), F32), space(m, d, H, Hp)
+
+    def call():
+        m.moonep_few_layer(d, H, Hp, X, ids, gates, w, out.view, ws.view)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    say("few_layer wide tiles captured", T)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        call()
+    for r in range(3):
+        X.copy_(rand_tensor((T, H), BF, 30 + r))
+        ids.copy_(i32(routing(T, E, K, 40 + r)[0]))
+        call()
+        torch.cuda.synchronize()
+        want = out.view.clone()
+        out.view.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view, want)
+    x, idn = np64(X), ids.cpu().numpy()
+    ref, size = few.few_layer(x, idn, np64(gates), np64(w))
+    scale = few.few_layer(np.abs(x), idn, np64(gates), np.abs(np64(w)))[0]
+    assert np.all(np.abs(np64(out.view) - ref) <= 2 * (H + K + 16) * U * scale)
+    assert out.intact() and ws.intact()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_no_tokens(m, bits):
+    L = m.MoeFew(2, 8, 0, 2, 64, 32, device=DEV, bits=bits, norm=True, router="sigmoid", router_bias=True)
+    say("MoeFew without tokens", bits)
+    L.forward()
+    torch.cuda.synchronize()
+    assert L.out.numel() == 0 and L.topk_idx.numel() == 0
+    F = m.MoeFFN(2, 8, 4, 0, 2, 64, 32, device=DEV, router="softmax", backward=True)
+    say("MoeFFN with a router without tokens")
+    F.forward()
+    F.backward()
+    torch.cuda.synchronize()
+    assert F.dlogits.numel() == 0
